@@ -501,6 +501,123 @@ int kv_state_append(const uint16_t* x, const uint16_t* gate, const uint16_t* win
                     int32_t m, void* stream);
 
 /* ------------------------------------------------------------------ */
+/* Paged serving: requests of different lengths over shared pages.        */
+/* ------------------------------------------------------------------ */
+/* The calls above keep one contiguous cache per sequence and, in the decode
+ * loop, move every sequence by one token.  The calls below serve requests
+ * that advance by different numbers of tokens per step (section 11's
+ * classical cache and state cache, split into pages): a pool of pages per
+ * layer, a block table per request, and a step plan built on the GPU from
+ * the request lengths.  The pages name no such layout; the stored bits and
+ * the attention rule are those of the calls above.
+ *
+ * A pool holds pages of page_size rows: entries as hca_kv_cache (B = pages,
+ * capacity = page_size), raw tokens as bf16 [pages][page_size][d].  Row i of
+ * request b is row i % page_size of page table[b][i / page_size].  A step
+ * has, per request b, ctx_len[b] tokens already cached and new tokens at
+ * positions ctx_len[b] .. ; the new tokens of all requests lie back to back
+ * in request order, request b's at rows row_start[b] .. row_start[b+1] - 1.
+ * All lengths live on the device, so that a captured step replays with the
+ * next step's lengths.  ctx_len + new_len stays below 2^31.  Integer arrays
+ * need their element's alignment only (a slice of a longer array will do).
+ *
+ * Each call is safe beside others on other streams and inside captured
+ * graphs as long as its outputs and workspace are its own. */
+typedef struct {
+    const int32_t* table;     /* [B][width] page numbers; outside [0, pages): no such page */
+    int32_t width;
+    int32_t page_size;        /* rows per page (any size >= 1)                 */
+    int64_t pages;            /* pages in the pool                             */
+} hca_page_map;
+
+/* Block tables and slot maps of one step.  Items are tokens (m = 1) or the
+ * entries of m tokens that the step completes: request b owns items
+ * [ctx_len / m, (ctx_len + new_len) / m).
+ *   ctx_len, new_len  int32 [B] (negative: taken as 0)
+ *   table       int32 [B][width], in and out: a page that the step needs first
+ *               (column c with ceil(lo / page_size) <= c < ceil(hi / page_size))
+ *               gets a fresh page number; other columns are left as they are
+ *   free_pages  int32 [free_cap]: a stack of free page numbers, its top at
+ *               free_count[0] - 1 (free_count int32 [1], on the device, taken
+ *               as free_cap when larger); pages are taken from the top in request order, then page
+ *               order.  Not changed: the count left goes to free_left.
+ *   row_start   int32 [B + 1] out: exclusive prefix sum of the item counts
+ *   row_req, row_pos  int32 [max_rows] out: request and item number of a row
+ *   slot        int64 [max_rows] out: row of the pool where the item goes,
+ *               page * page_size + item % page_size; -1 without a page (none
+ *               left, or beyond the table's width)
+ *   missing     int32 [1] out: pages that could not be given (0: all is well)
+ *   free_left   int32 [1] out: free pages left (the next step's free_count;
+ *               not the same address)
+ * Rows row_start[B] .. max_rows - 1 are left as they were; rows beyond
+ * max_rows are not written.  Supported: B <= 16384. */
+int kv_page_plan(const int32_t* ctx_len, const int32_t* new_len, int32_t B, int32_t m, int32_t page_size,
+                 int32_t* table, int32_t width, const int32_t* free_pages, const int32_t* free_count,
+                 int32_t free_cap, int64_t max_rows, int32_t* row_start, int32_t* row_req, int32_t* row_pos,
+                 int64_t* slot, int32_t* missing, int32_t* free_left, void* stream);
+
+/* New raw tokens into their pages: kv_token_prep (RMSNorm and partial RoPE at
+ * row_pos, section 9; ex == NULL or all-NULL members: a copy) with row t
+ * written to pool row slot[t].
+ *   x      bf16 [n_rows][d]; n_live int32 [1] on the device (row_start + B of
+ *          the plan): rows >= n_live[0] are skipped
+ *   slot   int64 [n_rows]; rows with a slot outside [0, n_slots) are skipped
+ *   pages  bf16 [n_slots][d] */
+int kv_page_store(const uint16_t* x, int64_t n_rows, const int32_t* n_live, const int32_t* row_pos,
+                  const int64_t* slot, hca_kv_layout layout, const hca_entry_extras* ex, uint16_t* pages,
+                  int64_t n_slots, void* stream);
+
+/* New blocks of m tokens (m = 4 or 128) pooled into entry pages, and the tail
+ * of each request's incomplete block kept (csa_compress / hca_compress and
+ * kv_state_append for requests of any lengths; the same bits).
+ *   x, gate    bf16 [n_tokens][d]: the step's raw tokens and gate logits
+ *   tok_start  int32 [B + 1]: their rows per request (row_start of a plan of
+ *              tokens); ctx_len int32 [B]
+ *   ent_*      row_start, row_req, row_pos, slot of a plan with this m
+ *              (max_entries rows: not fewer than the step's entries)
+ *   tail_x, tail_gate  bf16 [B][m][d], in and out: row t % m holds token t of
+ *              the incomplete block
+ *   pool       entry pages; n_slots = pages * page_size (pool.capacity is not read)
+ * An entry without a slot is not stored; its tokens still leave the tail. */
+int kv_page_compress(int32_t m, const uint16_t* x, const uint16_t* gate, int64_t n_tokens,
+                     const int32_t* tok_start, const int32_t* ctx_len, int32_t B, const float* pos_bias,
+                     const int32_t* ent_start, const int32_t* ent_req, const int32_t* ent_pos,
+                     const int64_t* ent_slot, int64_t max_entries, uint16_t* tail_x, uint16_t* tail_gate,
+                     hca_kv_layout layout, hca_kv_cache pool, int64_t n_slots, const hca_entry_extras* ex,
+                     void* stream);
+
+/* Attention of the step's new tokens over paged caches.  The query at position
+ * p = ctx_len[b] + i (row row_start[b] + i) sees, under one softmax,
+ *   paged_attn_chunk:   entries e < (p + 1) / m of its request, and its tokens
+ *                       max(0, p - W + 1) .. p
+ *   paged_attn_window:  its tokens max(0, p - W + 1) .. p, and its first
+ *                       tokens 0 .. n_first - 1 (those at or before p)
+ * with the attention rule of compressed_attn_prefill.  The step's own tokens
+ * and entries are in their pages already.  A key whose page the map does not
+ * hold is not visible; a query that sees no key gets 0.  A key that holds an
+ * infinity or a NaN (or a value beyond fp16's range, 65504) makes the outputs
+ * of the queries that see it NaN, and of no other.
+ *   q, out    bf16 [n_rows][H][d]; rows >= row_start[B] are left as they were
+ *   max_new   host bound of a request's new tokens (it chooses the kernels;
+ *             a wrong bound costs speed, not results); 0: n_rows
+ *   ex        q_norm_w, sink, inv_freq as in the calls above; q_pos and
+ *             win_len must be NULL (the positions are the step's)
+ *   ws        paged_attn_workspace_size(...) bytes, contents irrelevant
+ * Supported: layouts (512, 64, 64) and (128, 32, 32), 1 <= H <= 128, m >= 1,
+ * 1 <= W <= 4096, 0 <= n_first <= 4096. */
+size_t paged_attn_workspace_size(int64_t n_rows, int32_t B, int32_t H, hca_kv_layout layout, int64_t max_new,
+                                 int64_t max_entries, int32_t W, int32_t n_first);
+int paged_attn_chunk(const uint16_t* q, int64_t n_rows, int32_t H, int32_t B, const int32_t* row_start,
+                     const int32_t* ctx_len, int64_t max_new, int32_t m, hca_kv_layout layout, hca_kv_cache pool,
+                     hca_page_map entry_map, const uint16_t* pages, hca_page_map token_map, int32_t W,
+                     float softmax_scale, const hca_attn_extras* ex, uint16_t* out, void* ws, size_t ws_bytes,
+                     void* stream);
+int paged_attn_window(const uint16_t* q, int64_t n_rows, int32_t H, int32_t B, const int32_t* row_start,
+                      const int32_t* ctx_len, int64_t max_new, hca_kv_layout layout, const uint16_t* pages,
+                      hca_page_map token_map, int32_t W, int32_t n_first, float softmax_scale,
+                      const hca_attn_extras* ex, uint16_t* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------ */
 /* One decode step from host memory to host memory (sections 7 and 8:    */
 /* the CSA path and the HCA path of one decode position).               */
 /* ------------------------------------------------------------------ */

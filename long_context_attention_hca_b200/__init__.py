@@ -38,6 +38,8 @@ EXPORTED = (
     "kv_state_append", "csa_compress_overlap", "indexer_key_compress",
     "lightning_index_ex", "topk_select_ex_workspace_size", "topk_select_ex",
     "lightning_index_topk_ex_workspace_size", "lightning_index_topk_ex", "hca_decode_step_host",
+    "kv_page_plan", "kv_page_store", "kv_page_compress", "paged_attn_workspace_size", "paged_attn_chunk",
+    "paged_attn_window",
 )
 
 
@@ -280,6 +282,24 @@ class KVCache:
 
     def nbytes(self) -> int:
         return sum(t.numel() * t.element_size() for t in (self.codes, self.scales, self.rope))
+
+    @classmethod
+    def of(cls, codes, scales, rope) -> "KVCache":
+        """The cache that these tensors hold (no copy), e.g. a pool of entry
+        pages: codes [pages][page_size][d-d_rope], scales, rope likewise."""
+        for t, dt, n in ((codes, torch.uint8, "codes"), (scales, torch.float32, "scales"),
+                         (rope, torch.bfloat16, "rope")):
+            _need(t, dt, n)
+        if codes.dim() != 3 or not (codes.shape[:2] == scales.shape[:2] == rope.shape[:2]):
+            raise ValueError("codes, scales, rope: [B][capacity][...] of the same B and capacity")
+        dn, dr = codes.shape[2], rope.shape[2]
+        layout = {(448, 64): LAYOUT_512, (96, 32): LAYOUT_128}.get((dn, dr))
+        if layout is None or scales.shape[2] != dn // layout[2]:
+            raise ValueError("codes, scales, rope: not a supported layout")
+        v = cls.__new__(cls)
+        v.B, v.capacity, v.layout = codes.shape[0], codes.shape[1], layout
+        v.codes, v.scales, v.rope = codes, scales, rope
+        return v
 
     def sequence(self, b: int) -> "KVCache":
         """View of one sequence as a B = 1 cache (no copy)."""
@@ -535,3 +555,6 @@ def indexer_key_compress(xa, za, xb, zb, pos_bias, n_blocks, k_codes, k_sf, entr
                                      _p(pos_bias), B, n_blocks, c, _p(k_codes), _p(k_sf), k_codes.shape[1],
                                      entry_begin, _stream(stream)), "indexer_key_compress")
 
+
+from .paged import (PagePlan, kv_page_compress, kv_page_plan, kv_page_store, paged_attn_chunk,  # noqa: E402,F401
+                    paged_attn_window, paged_attn_workspace_size)

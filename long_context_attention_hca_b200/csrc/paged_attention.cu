@@ -1,0 +1,528 @@
+// paged_attention.cu -- attention of each request's new tokens over its paged
+// cache: the compressed entries of complete blocks, the sliding window of its
+// raw tokens and, where asked, its first tokens, under one softmax; requests of
+// any length, from one new token (decode) to a prefill chunk.
+//
+// "DeepSeek V4 ..." reading note, sections 7 and 8 (shared key-value MQA, the
+// window branch, dense attention over every compressed entry), 9 (FP8 entries
+// with BF16 RoPE dims; query RMSNorm, partial RoPE, sink) and the section 8
+// table (ratio 0: window only).
+//
+//   o_h(p) = sum_j w_j k_j / (sum_j w_j [+ e^sink_h]),  w_j = e^(scale q_h.k_j)
+//   over j: entries e < (p + 1) / m, tokens max(0, p - W + 1) .. p, tokens
+//   below n_first; key = value, shared by every head.
+#include "paged_attention.cuh"
+
+namespace hca {
+namespace paged {
+
+// ---------------------------------------------------------------- row kernel
+// One CTA = one tile of R rows (tokens x heads, flattened inside a request) and
+// one split of its keys.  8 warps: R / 16 row groups x KG key groups; warp
+// (rg, kg) computes S for 16 rows and its TK / KG keys over all D dims (mma.sync,
+// fp16 operands, fp32 sums), the groups share row maxima and P through shared
+// memory, and warp (rg, kg) then accumulates its D / KG dims of O in registers.
+// Keys cross from their pages as stored and become fp16 in shared memory.
+//
+// A key that holds an infinity or a NaN (or a value beyond fp16's range) is
+// stored as zeros and marked: a query that sees it gets NaN, one that does not
+// see it is untouched (0 x NaN would not be).
+template <int D, int R>
+struct Rows {
+    static constexpr int RG = R / 16, KG = 8 / RG;
+    static constexpr int KEYS = TK / KG;         // keys of a warp's S
+    static constexpr int NT = KEYS / 8;          // its n-tiles
+    static constexpr int DW = D / KG;            // output dims of a warp
+    static constexpr int NO = DW / 8;            // their n-tiles
+    static constexpr int DR = D == 512 ? 64 : 32;
+    static constexpr int G = D == 512 ? 64 : 32;
+    static constexpr int DN = D - DR;
+    static constexpr size_t Q_BYTES = size_t(R) * D * 2;
+    static constexpr size_t K_BYTES = size_t(TK) * D * 2;
+    static constexpr size_t P_BYTES = size_t(R) * TK * 2;
+    static constexpr size_t CS_BYTES = size_t(R) * (DR / 2) * 8;     // cos / sin of each row's position
+    static constexpr size_t SMEM = Q_BYTES + K_BYTES + P_BYTES + CS_BYTES;
+};
+
+// row-major fp16 tile, 16-byte chunks XOR-swizzled by row (conflict-free ldmatrix)
+template <int W2>
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return static_cast<uint32_t>(row * W2 + ((chunk ^ (row & 7)) << 4));
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
+    return pack_half2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+}
+
+template <int D, int R>
+__global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
+    using C = Rows<D, R>;
+    extern __shared__ __align__(128) char smem[];
+    char* qs = smem;
+    char* ks = smem + C::Q_BYTES;
+    char* ps = ks + C::K_BYTES;
+    float2* s_cs = reinterpret_cast<float2*>(ps + C::P_BYTES);
+    __shared__ float s_max[8][16];               // [warp][row of its group]
+    __shared__ float s_l[8][16];
+    __shared__ float s_add[TK];                  // -inf: no such key; NaN: the key holds a non-finite value
+    const uint32_t qa = static_cast<uint32_t>(__cvta_generic_to_shared(qs));
+    const uint32_t ka = static_cast<uint32_t>(__cvta_generic_to_shared(ks));
+    const uint32_t pa = static_cast<uint32_t>(__cvta_generic_to_shared(ps));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rg = warp / C::KG, kg = warp % C::KG;
+    const int split = blockIdx.y;
+
+    Tile T;
+    if (!make_tile(p, blockIdx.x, R, T) || T.n_new >= p.min_chunk) return;
+    const int n_tiles = (T.n_tot + TK - 1) / TK;
+    const int t_begin = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.n_splits);
+    const int t_end = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.n_splits);
+
+    // ---- queries -> fp16 (rows past the last are zero); RMSNorm and RoPE in fp32
+    if (p.inv_freq) {
+        for (int w = tid; w < T.rows * (C::DR / 2); w += 256) {
+            const int r = w / (C::DR / 2);
+            // one table row per token: rows of the same token read the first one's
+            if (r == 0 || (T.r0 + r) % p.H == 0)
+                s_cs[w] = rope_cs(p.inv_freq, w % (C::DR / 2), T.ctx + (T.r0 + r) / p.H);
+        }
+        __syncthreads();
+    }
+    for (int r = warp; r < R; r += 8) {
+        constexpr int CL = D / 32;               // consecutive dims of a lane
+        uint32_t v[CL / 2];
+#pragma unroll
+        for (int i = 0; i < CL / 2; ++i) v[i] = 0;
+        if (r < T.rows) {
+            const uint16_t* src = p.q + (T.row0 + r) * D + lane * CL;
+            if constexpr (CL >= 8) {
+#pragma unroll
+                for (int i = 0; i < CL / 8; ++i)
+                    *reinterpret_cast<uint4*>(v + 4 * i) = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            } else {
+                *reinterpret_cast<uint2*>(v) = __ldg(reinterpret_cast<const uint2*>(src));
+            }
+        }
+        float f[CL];
+#pragma unroll
+        for (int i = 0; i < CL / 2; ++i) {
+            f[2 * i] = __uint_as_float(v[i] << 16);
+            f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+        }
+        if (p.q_norm_w && r < T.rows) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < CL; ++i) ss += f[i] * f[i];
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
+#pragma unroll
+            for (int i = 0; i < CL; ++i) f[i] = f[i] * rr * __ldg(p.q_norm_w + lane * CL + i);
+        }
+        if (p.inv_freq && r < T.rows && lane * CL >= C::DN) {
+            const int h = (T.r0 + r) % p.H;
+            const float2* cs = s_cs + max(r - h, 0) * (C::DR / 2) + (lane * CL - C::DN) / 2;
+#pragma unroll
+            for (int i = 0; i < CL / 2; ++i) {
+                const float a = f[2 * i], b = f[2 * i + 1];
+                f[2 * i] = a * cs[i].x - b * cs[i].y;
+                f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
+            }
+        }
+        uint32_t h2[CL / 2];
+#pragma unroll
+        for (int i = 0; i < CL / 2; ++i) h2[i] = pack_half2(f[2 * i], f[2 * i + 1]);
+        if constexpr (CL >= 8) {
+#pragma unroll
+            for (int i = 0; i < CL / 8; ++i)
+                *reinterpret_cast<uint4*>(qs + swz<D * 2>(r, lane * (CL / 8) + i)) = *reinterpret_cast<uint4*>(h2 + 4 * i);
+        } else {
+            *reinterpret_cast<uint2*>(qs + swz<D * 2>(r, lane / 2) + (lane & 1) * 8) = *reinterpret_cast<uint2*>(h2);
+        }
+    }
+
+    // this thread's rows of S: g8 and g8 + 8 of its row group
+    const int g8 = lane >> 2, q4 = lane & 3;
+    RowKeys rk[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = min(rg * 16 + g8 + 8 * i, T.rows - 1);
+        rk[i] = row_keys(p, T, T.ctx + (T.r0 + r) / p.H);
+    }
+    float o[C::NO][4];
+#pragma unroll
+    for (int j = 0; j < C::NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+    float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.0f, 0.0f};
+
+    constexpr int UPK = D / 16;                  // 16-dim units of a key
+    constexpr int KPP = 256 / UPK;               // keys per pass
+    const int u = tid % UPK, kr = tid / UPK, d0 = u * 16;
+    for (int t = t_begin; t < t_end; ++t) {
+        __syncthreads();                         // the last tile's keys and P are read
+        bool flagged = false;
+#pragma unroll
+        for (int k0 = 0; k0 < TK; k0 += KPP) {
+            const int key = k0 + kr, slot = t * TK + key;
+            uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            int64_t row = -1;
+            if (slot < T.n_e) {
+                row = entry_row(p, T.b, slot);
+                if (row >= 0) {
+                    if (d0 < C::DN) {
+                        const uint4 cv = __ldg(reinterpret_cast<const uint4*>(p.codes + row * C::DN + d0));
+                        const float sc = __ldg(p.scales + row * (C::DN / C::G) + d0 / C::G);
+                        const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] & 0xFFFFu)));
+                            const float2 b = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] >> 16)));
+                            h[2 * i] = pack_half2(a.x * sc, a.y * sc);
+                            h[2 * i + 1] = pack_half2(b.x * sc, b.y * sc);
+                        }
+                    } else {
+                        const uint4* rp = reinterpret_cast<const uint4*>(p.rope + row * C::DR + (d0 - C::DN));
+                        const uint4 v0 = __ldg(rp), v1 = __ldg(rp + 1);
+                        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
+                    }
+                }
+            } else if (slot < T.n_tot) {
+                const int j = slot - T.n_e;
+                row = token_row(p, T.b, static_cast<uint32_t>(j < T.n_f ? j : T.w_lo + (j - T.n_f)));
+                if (row >= 0) {
+                    const uint4* rp = reinterpret_cast<const uint4*>(p.tok + row * D + d0);
+                    const uint4 v0 = __ldg(rp), v1 = __ldg(rp + 1);
+                    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
+                }
+            }
+            bool bad = false;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) bad = bad || bad_half2(h[i]);
+            // the UPK lanes of a key are one warp's (8 or 32 consecutive lanes)
+            const unsigned bm = __ballot_sync(0xffffffffu, bad) >> (UPK == 32 ? 0 : (lane / UPK) * UPK);
+            const bool kbad = (bm & (UPK == 32 ? 0xffffffffu : (1u << (UPK & 31)) - 1u)) != 0;
+            if (kbad)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = 0;
+            *reinterpret_cast<uint4*>(ks + swz<D * 2>(key, 2 * u)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(ks + swz<D * 2>(key, 2 * u + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
+            if (u == 0) s_add[key] = row < 0 ? -INFINITY : (kbad ? __int_as_float(0x7fc00000) : 0.0f);
+            flagged = flagged || kbad || (row < 0 && slot < T.n_tot);
+        }
+        flagged = __syncthreads_or(flagged);
+
+        // ---- S = Q K^T for 16 rows and this warp's keys
+        float s[C::NT][4];
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+        const int mi = lane >> 3;
+#pragma unroll 8
+        for (int kk = 0; kk < D / 16; ++kk) {
+            uint32_t a[4];
+            ldsm4(qa + swz<D * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
+            if constexpr (C::NT >= 2) {
+#pragma unroll
+                for (int nt = 0; nt < C::NT; nt += 2) {
+                    uint32_t b[4];
+                    ldsm4(ka + swz<D * 2>(kg * C::KEYS + nt * 8 + (lane & 7) + 8 * (mi >> 1), 2 * kk + (mi & 1)), b);
+                    mma16816(s[nt], a, b[0], b[1]);
+                    mma16816(s[nt + 1], a, b[2], b[3]);
+                }
+            } else {
+                // 8 keys: one x4 load brings two k-steps; the odd step uses the pair loaded with the even one
+                uint32_t b[4];
+                ldsm4(ka + swz<D * 2>(kg * 8 + (lane & 7), (2 * (kk & ~1) + mi)), b);
+                mma16816(s[0], a, (kk & 1) ? b[2] : b[0], (kk & 1) ? b[3] : b[1]);
+            }
+        }
+        // ---- logits (base 2), masks, row maxima over the key groups
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int key = kg * C::KEYS + j * 8 + q4 * 2 + (i & 1);
+                float v = s[j][i] * p.scale_log2;
+                if (flagged) v += s_add[key];
+                if (!sees(rk[i >> 1], T.n_e, t * TK + key)) v = -INFINITY;
+                s[j][i] = v;
+                mx[i >> 1] = fmaxf(mx[i >> 1], v);
+            }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        }
+        if (q4 == 0) { s_max[warp][g8] = mx[0]; s_max[warp][g8 + 8] = mx[1]; }
+        __syncthreads();
+        float alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mn = m_r[i];
+#pragma unroll
+            for (int k = 0; k < C::KG; ++k) mn = fmaxf(mn, s_max[rg * C::KG + k][g8 + 8 * i]);
+            // nothing seen yet: any finite reference does (every term is 0)
+            alpha[i] = mn == -INFINITY ? 1.0f : ex2(m_r[i] - mn);
+            m_r[i] = mn;
+        }
+        float rs[2] = {0.0f, 0.0f};
+        const float ref[2] = {m_r[0] == -INFINITY ? 0.0f : m_r[0], m_r[1] == -INFINITY ? 0.0f : m_r[1]};
+#pragma unroll
+        for (int j = 0; j < C::NT; ++j) {
+            const uint32_t lo = pack_half2(ex2(s[j][0] - ref[0]), ex2(s[j][1] - ref[0]));
+            const uint32_t hi = pack_half2(ex2(s[j][2] - ref[1]), ex2(s[j][3] - ref[1]));
+            // l sums the probabilities as PV uses them: fp16, at most half a step off each
+            const float2 fl = unpack_half2(lo), fh = unpack_half2(hi);
+            rs[0] += fl.x + fl.y;
+            rs[1] += fh.x + fh.y;
+            const int col = kg * C::KEYS + j * 8 + q4 * 2;
+            const int r = rg * 16 + g8;
+            *reinterpret_cast<uint32_t*>(ps + swz<TK * 2>(r, col >> 3) + (col & 7) * 2) = lo;
+            *reinterpret_cast<uint32_t*>(ps + swz<TK * 2>(r + 8, col >> 3) + (col & 7) * 2) = hi;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) l_r[i] = l_r[i] * alpha[i] + rs[i];
+#pragma unroll
+        for (int j = 0; j < C::NO; ++j) {
+            o[j][0] *= alpha[0]; o[j][1] *= alpha[0];
+            o[j][2] *= alpha[1]; o[j][3] *= alpha[1];
+        }
+        __syncthreads();                         // P is complete
+        // ---- O += P V (the same tile), this warp's dims
+#pragma unroll
+        for (int kk = 0; kk < TK / 16; ++kk) {
+            uint32_t a[4];
+            ldsm4(pa + swz<TK * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
+#pragma unroll
+            for (int nt = 0; nt < C::NO; nt += 2) {
+                uint32_t b[4];
+                ldsm4t(ka + swz<D * 2>(kk * 16 + (lane & 7) + 8 * (mi & 1), kg * (C::DW / 8) + nt + (mi >> 1)), b);
+                mma16816(o[nt], a, b[0], b[1]);
+                mma16816(o[nt + 1], a, b[2], b[3]);
+            }
+        }
+    }
+
+    // ---- l over the key groups
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l_r[i] += __shfl_xor_sync(0xffffffffu, l_r[i], 1);
+        l_r[i] += __shfl_xor_sync(0xffffffffu, l_r[i], 2);
+    }
+    if (q4 == 0) { s_l[warp][g8] = l_r[0]; s_l[warp][g8 + 8] = l_r[1]; }
+    __syncthreads();
+    float inv[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = rg * 16 + g8 + 8 * i;
+        float l = 0.0f;
+#pragma unroll
+        for (int k = 0; k < C::KG; ++k) l += s_l[rg * C::KG + k][g8 + 8 * i];
+        l_r[i] = l;
+        if (p.n_splits == 1 && p.sink && r < T.rows) {
+            // no key seen: the sink alone, the output is 0
+            if (m_r[i] != -INFINITY || l != l) l += ex2(__ldg(p.sink + (T.r0 + r) % p.H) * LOG2E - m_r[i]);
+        }
+        inv[i] = l == 0.0f ? 0.0f : 1.0f / l;
+    }
+    const int64_t part = static_cast<int64_t>(blockIdx.x) * p.n_splits + split;
+    if (p.n_splits > 1 && kg == 0 && q4 == 0) {
+        float* ml = p.part_ml + part * 2 * R + rg * 16 + g8;
+        ml[0] = m_r[0]; ml[8] = m_r[1];
+        ml[R] = l_r[0]; ml[R + 8] = l_r[1];
+    }
+#pragma unroll
+    for (int j = 0; j < C::NO; ++j) {
+        const int d = kg * C::DW + j * 8 + q4 * 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = rg * 16 + g8 + 8 * i;
+            if (r >= T.rows) continue;
+            float x = o[j][2 * i] * inv[i], y = o[j][2 * i + 1] * inv[i];
+            if (p.n_splits > 1) {
+                *reinterpret_cast<uint32_t*>(p.part_o + (part * R + r) * D + d) = pack_half2(x, y);
+            } else {
+                if (p.inv_freq && d >= C::DN) {
+                    const int h = (T.r0 + r) % p.H;
+                    const float2 cs = s_cs[max(r - h, 0) * (C::DR / 2) + (d - C::DN) / 2];
+                    const float x2 = x * cs.x + y * cs.y, y2 = y * cs.x - x * cs.y;
+                    x = x2; y = y2;
+                }
+                *reinterpret_cast<__nv_bfloat162*>(p.out + (T.row0 + r) * D + d) = __floats2bfloat162_rn(x, y);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- combine
+// Joins a tile's splits: out = sum_s 2^(m_s - M) l_s o_s / (sum_s 2^(m_s - M)
+// l_s [+ sink]), o_s = O_s / l_s in fp16 (half the traffic of fp32; 2^-12
+// relative, an eighth of the output's bf16 step).  A warp per row, its lanes
+// over the dims; lanes 0..S-1 (twice for S > 32) hold the weights.
+template <int D, int R>
+__global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
+    constexpr int DR = D == 512 ? 64 : 32, DN = D - DR, CL = D / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();                                  // the partials are complete
+    Tile T;
+    if (!make_tile(p, blockIdx.x, R, T) || T.n_new >= p.min_chunk) return;
+    const int r = blockIdx.y * 8 + warp;
+    if (r >= T.rows) return;
+    const int S = p.n_splits;
+    const int64_t part = static_cast<int64_t>(blockIdx.x) * S;
+    float m[2], l[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const int s = lane + 32 * k;
+        m[k] = s < S ? p.part_ml[(part + s) * 2 * R + r] : -INFINITY;
+        l[k] = s < S ? p.part_ml[(part + s) * 2 * R + R + r] : 0.0f;
+    }
+    float M = fmaxf(m[0], m[1]);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float w[2], L = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        // a split that saw nothing has l = 0 and an O that is not read; l = NaN stays NaN
+        w[k] = l[k] == 0.0f ? 0.0f : (M == -INFINITY ? l[k] : ex2(m[k] - M) * l[k]);
+        L += w[k];
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    const int h = (T.r0 + r) % p.H;
+    if (p.sink && (M != -INFINITY || L != L)) L += ex2(__ldg(p.sink + h) * LOG2E - M);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+    float acc[CL];
+#pragma unroll
+    for (int i = 0; i < CL; ++i) acc[i] = 0.0f;
+    for (int s = 0; s < S; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
+        if (ws == 0.0f) continue;
+        const uint16_t* src = p.part_o + ((part + s) * R + r) * D + lane * CL;
+        uint32_t v[CL / 2];
+        if constexpr (CL >= 8) {
+#pragma unroll
+            for (int i = 0; i < CL / 8; ++i)
+                *reinterpret_cast<uint4*>(v + 4 * i) = *(reinterpret_cast<const uint4*>(src) + i);
+        } else {
+            *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(src);
+        }
+#pragma unroll
+        for (int i = 0; i < CL / 2; ++i) {
+            const float2 f = unpack_half2(v[i]);
+            acc[2 * i] += ws * f.x;
+            acc[2 * i + 1] += ws * f.y;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < CL; ++i) acc[i] *= inv;
+    if (p.inv_freq && lane * CL >= DN) {
+        const int64_t pos = T.ctx + (T.r0 + r) / p.H;
+#pragma unroll
+        for (int i = 0; i < CL / 2; ++i) {
+            const float2 cs = rope_cs(p.inv_freq, (lane * CL - DN) / 2 + i, pos);
+            const float x = acc[2 * i], y = acc[2 * i + 1];
+            acc[2 * i] = x * cs.x + y * cs.y;
+            acc[2 * i + 1] = y * cs.x - x * cs.y;
+        }
+    }
+    uint32_t v[CL / 2];
+#pragma unroll
+    for (int i = 0; i < CL / 2; ++i) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(acc[2 * i], acc[2 * i + 1]);
+        v[i] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    uint16_t* dst = p.out + (T.row0 + r) * D + lane * CL;
+    if constexpr (CL >= 8) {
+#pragma unroll
+        for (int i = 0; i < CL / 8; ++i) *(reinterpret_cast<uint4*>(dst) + i) = *reinterpret_cast<uint4*>(v + 4 * i);
+    } else {
+        *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(v);
+    }
+}
+
+// ---------------------------------------------------------------- host side
+// Rows of a tile: 16 when no request can fill more (a small head count at
+// decode), else 64.
+inline int tile_rows(int64_t max_new, int H) { return max_new * H <= 16 ? 16 : 64; }
+inline int64_t tile_count(int64_t n_rows, int H, int B, int R) { return n_rows * H / R + B; }
+
+// Splits: enough CTAs for every SM when the tiles alone are too few, but at
+// least two key tiles for each (max_keys: the longest key list there can be).
+inline int split_count(int64_t tiles, int64_t max_keys) {
+    int64_t s = sm_count() / (tiles > 0 ? tiles : 1);
+    const int64_t by_len = ceil_div(ceil_div(max_keys, TK), 2);
+    if (s > by_len) s = by_len;
+    if (s > MAX_SPLITS) s = MAX_SPLITS;
+    return s < 1 ? 1 : static_cast<int>(s);
+}
+
+struct Plan { int R, splits; int64_t tiles; };
+
+static Plan make_plan(int64_t n_rows, int B, int H, int64_t max_new, int64_t max_keys) {
+    Plan k;
+    // n_rows rows over B requests: a tile for each request at least, whatever the lengths
+    k.R = tile_rows(max_new, H);
+    k.tiles = tile_count(n_rows, H, B, k.R);
+    // tiles that can hold rows: every request's rows, rounded up
+    const int64_t busy = n_rows * H / k.R + (n_rows < B ? n_rows : B);
+    k.splits = split_count(n_rows * H <= static_cast<int64_t>(B) * k.R ? (n_rows < B ? n_rows : B) : busy, max_keys);
+    return k;
+}
+
+template <int D, int R>
+static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
+    auto kern = paged_rows_kernel<D, R>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Rows<D, R>::SMEM));
+    if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
+    kern<<<dim3(static_cast<unsigned>(k.tiles), k.splits), 256, Rows<D, R>::SMEM, st>>>(p);
+    HCA_CHECK_LAUNCH();
+    if (k.splits > 1) {
+        e = launch_pdl(paged_combine_kernel<D, R>, dim3(static_cast<unsigned>(k.tiles), R / 8), dim3(256), 0, st, p);
+        if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
+        HCA_CHECK_LAUNCH();
+    }
+    return HCA_OK;
+}
+
+}  // namespace paged
+
+size_t paged_attn_ws_bytes(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_keys) {
+    const paged::Plan k = paged::make_plan(n_rows, B, H, max_new, max_keys);
+    if (k.splits <= 1) return 0;
+    return static_cast<size_t>(k.tiles) * k.splits * k.R * (static_cast<size_t>(D) * 2 + 2 * sizeof(float)) + 256;
+}
+
+int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_keys, void* ws, size_t ws_bytes,
+                      cudaStream_t st) {
+    const paged::Plan k = paged::make_plan(p.n_rows, p.B, p.H, max_new, max_keys);
+    p.n_splits = k.splits;
+    p.min_chunk = 0x7FFFFFFF;
+    if (k.splits > 1) {
+        if (ws == nullptr || ws_bytes < paged_attn_ws_bytes(p.n_rows, p.B, p.H, D, max_new, max_keys))
+            return HCA_ERR_WORKSPACE;
+        p.part_o = static_cast<uint16_t*>(ws);
+        p.part_ml = reinterpret_cast<float*>(p.part_o + static_cast<size_t>(k.tiles) * k.splits * k.R * D);
+    }
+    if (D == 512)
+        return k.R == 16 ? paged::launch_rows<512, 16>(p, k, st) : paged::launch_rows<512, 64>(p, k, st);
+    return k.R == 16 ? paged::launch_rows<128, 16>(p, k, st) : paged::launch_rows<128, 64>(p, k, st);
+}
+
+}  // namespace hca

@@ -585,5 +585,127 @@ class DecodeLoop:
         return self.out
 
 
+# ------------------------------------------------------------------ paged serving loop
+@dataclasses.dataclass
+class PagedLayer:
+    """One layer of a PagedLoop: its token pages, and for ratio 128 its entry
+    pages and the tail of every request's incomplete block."""
+    ratio: int                                  # 0 (window and first tokens) or 128 (HCA)
+    pages: torch.Tensor                         # [token pages][page_size][d] bf16
+    cache: Optional[KVCache] = None             # entry pages
+    tail_x: Optional[torch.Tensor] = None       # [B][128][d]
+    tail_gate: Optional[torch.Tensor] = None
+    bias: Optional[torch.Tensor] = None         # [128][d]
+    entry_extras: object = None
+    attn_extras: object = None
+
+
+class PagedLoop:
+    """Steps of a batch of requests of different lengths over paged caches:
+    any mix of prefill chunks, single tokens and idle requests per step.  Per
+    step the token and entry plans are built on the GPU from the lengths
+    (kv_page_plan; one block table serves every layer's pool), then each layer
+    stores its new tokens (kv_page_store), pools the blocks that complete
+    (kv_page_compress) and attends: HCA layers to every complete entry and the
+    window (paged_attn_chunk), ratio-0 layers to the window and the first
+    n_first tokens (paged_attn_window).  No length is read by the host, so a
+    step can be captured and replayed with other lengths."""
+
+    def __init__(self, B: int, H: int, layout, ratios: List[int], W: int, n_first: int, max_tokens: int,
+                 max_rows: int, softmax_scale: float, token_page: int = 64, entry_page: int = 64,
+                 token_pages: Optional[int] = None, entry_pages: Optional[int] = None, device="cuda",
+                 s9: Optional[List[dict]] = None):
+        """max_tokens: bound of a request's length; max_rows: bound of a step's
+        new tokens; token_pages, entry_pages: pool sizes (default: room for B
+        requests of max_tokens)."""
+        from . import AttnExtras, EntryExtras, PagePlan
+        if any(r not in (0, HCA_RATIO) for r in ratios):
+            raise ValueError("PagedLoop: layers of ratio 0 and 128")
+        d = layout[0]
+        dev = torch.device(device)
+        self.B, self.H, self.layout, self.W, self.n_first, self.scale = B, H, tuple(layout), W, n_first, softmax_scale
+        self.token_page, self.entry_page = token_page, entry_page
+        width_t = max(1, -(-max_tokens // token_page))
+        width_e = max(1, -(-(max_tokens // HCA_RATIO) // entry_page))
+        n_t = B * width_t if token_pages is None else token_pages
+        n_e = B * width_e if entry_pages is None else entry_pages
+        i32 = dict(dtype=torch.int32, device=dev)
+        self.ctx = torch.zeros((B,), **i32)
+        self.token_table = torch.full((B, width_t), -1, **i32)
+        self.entry_table = torch.full((B, width_e), -1, **i32)
+        self.free_tokens, self.free_entries = torch.arange(n_t, **i32), torch.arange(n_e, **i32)
+        self.n_free_tokens = torch.full((1,), n_t, **i32)
+        self.n_free_entries = torch.full((1,), n_e, **i32)
+        self.token_plan = PagePlan.empty(B, max_rows, dev)
+        # every request may complete a block with its first new token
+        self.entry_plan = PagePlan.empty(B, B + max_rows // HCA_RATIO, dev)
+        self.short = torch.zeros((1,), **i32)            # pages that could not be given, over all steps
+        self.layers: List[PagedLayer] = []
+        for li, r in enumerate(ratios):
+            P = s9[li] if s9 is not None else None
+            L = PagedLayer(r, torch.zeros((n_t, token_page, d), dtype=torch.bfloat16, device=dev))
+            if P is not None:
+                L.entry_extras = EntryExtras(P["kv_norm_w"], P["eps"], P["inv_freq"])
+                L.attn_extras = AttnExtras(P["q_norm_w"], P["eps"], P["sink"], P["inv_freq"])
+            if r > 0:
+                L.cache = KVCache(n_e, entry_page, layout, device=dev, zero=True)
+                L.tail_x = torch.zeros((B, r, d), dtype=torch.bfloat16, device=dev)
+                L.tail_gate = torch.zeros((B, r, d), dtype=torch.bfloat16, device=dev)
+            self.layers.append(L)
+
+    def set_bias(self, li: int, bias: torch.Tensor):
+        """HCA layer li: the compressor's positional bias [128][d]."""
+        self.layers[li].bias = bias
+
+    def step(self, new_len: torch.Tensor, x_new: List[torch.Tensor], gate_new: List[Optional[torch.Tensor]],
+             q: List[torch.Tensor], max_new: Optional[int] = None):
+        """One step: new_len int32 [B] on the device; per layer the new tokens'
+        raw KV x_new[li] and gate logits gate_new[li] [n][d] (gates of HCA
+        layers only are read) and queries q[li] [n][H][d], request after
+        request; max_new: host bound of a request's new tokens.  Returns the
+        per-layer outputs [n][H][d]."""
+        from . import kv_page_compress, kv_page_plan, kv_page_store, paged_attn_chunk, paged_attn_window
+        tp, ep = self.token_plan, self.entry_plan
+        kv_page_plan(self.ctx, new_len, 1, self.token_page, self.token_table, self.free_tokens, self.n_free_tokens,
+                     plan=tp)
+        kv_page_plan(self.ctx, new_len, HCA_RATIO, self.entry_page, self.entry_table, self.free_entries,
+                     self.n_free_entries, plan=ep)
+        outs = []
+        for li, L in enumerate(self.layers):
+            kv_page_store(x_new[li], tp, L.pages, self.layout, extras=L.entry_extras)
+            if L.ratio > 0:
+                kv_page_compress(x_new[li], gate_new[li], L.bias, tp.row_start, self.ctx, ep, L.tail_x, L.tail_gate,
+                                 L.cache, extras=L.entry_extras)
+                outs.append(paged_attn_chunk(q[li], tp.row_start, self.ctx, L.ratio, L.cache, self.entry_table, L.pages,
+                                             self.token_table, self.W, self.scale, max_new=max_new,
+                                             extras=L.attn_extras))
+            else:
+                outs.append(paged_attn_window(q[li], tp.row_start, self.ctx, L.pages, self.token_table, self.W,
+                                              self.n_first, self.scale, max_new=max_new, extras=L.attn_extras))
+        self.n_free_tokens.copy_(tp.free_left)
+        self.n_free_entries.copy_(ep.free_left)
+        self.short.add_(tp.missing).add_(ep.missing)
+        self.ctx.add_(new_len)
+        return outs
+
+    def missing(self) -> int:
+        """Pages that the steps so far wanted and the pools could not give (the
+        tokens and entries without a page are not visible).  Synchronises."""
+        return int(self.short.item())
+
+    def release(self, b: int):
+        """Request b is done: its pages go back to the free stacks, its slot
+        starts again at length 0.  Synchronises."""
+        for table, free, count in ((self.token_table, self.free_tokens, self.n_free_tokens),
+                                   (self.entry_table, self.free_entries, self.n_free_entries)):
+            row = table[b]
+            back = row[row >= 0]
+            n = int(count.item())
+            free[n:n + back.numel()] = back
+            count.fill_(n + back.numel())
+            row.fill_(-1)
+        self.ctx[b] = 0
+
+
 def r_is_csa(ratio: int) -> bool:
     return ratio == CSA_RATIO

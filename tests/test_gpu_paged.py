@@ -1,0 +1,630 @@
+"""Paged serving calls against the oracle and plain restatements: block tables
+and slot maps, token and entry stores (bit for bit), attention of ragged chunks
+and single tokens over pages, and steps of all of them together.
+
+Attention tolerance, per output element, from the roundings on the way (u16 =
+2^-11, half a step of fp16; ub = 2^-8, half a step of bf16): a key is rounded
+to fp16 once and the query once, so a logit is off by at most
+dl = scale * sum_i |q_i| |k_i| * (2 u16 + 2^-14), the last term covering the
+fp32 sum of d <= 512 products (512 * 2^-23 = 2^-14 where every addition
+truncates), plus 2^-12 for values below fp16's normal range (2^-25 off each);
+a weight is then off by a factor within e^(+-2 dl) and P by u16 more, the
+values by u16, a split's partial by u16: |error| <= (e^(2 dl) - 1 + 4 u16) *
+sum_j p_j |v_j| + ub |o|.  That is a worst case; the mean is held to what the
+workloads are held to: sum |a - b| / sum |b| <= 1e-3 for the arithmetic plus
+2^-9, the mean of a bf16 rounding (half of its largest).
+"""
+import numpy as np
+import pytest
+import torch
+
+import hca_inputs as inp
+import oracle
+from gpu_util import host
+
+pytestmark = pytest.mark.gpu
+
+hca = pytest.importorskip("long_context_attention_hca_b200")
+
+DEV = "cuda"
+LAYOUTS = {512: (512, 64, 64), 128: (128, 32, 32)}
+U16, UB = 2.0 ** -11, 2.0 ** -8
+
+
+def gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    return g
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device=DEV)
+
+
+def bf(shape, g, std=1.0):
+    return (torch.randn(shape, generator=g, device=DEV) * std).to(torch.bfloat16)
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ------------------------------------------------------------------ plan
+def plan_ref(ctx, new, m, P, table, free, n_free):
+    """Request by request, item by item."""
+    table = table.copy()
+    free = list(free[:n_free])
+    width = table.shape[1]
+    start, req, pos, slot, missing = [0], [], [], [], 0
+    for b, (c, n) in enumerate(zip(ctx, new)):
+        c, n = max(c, 0), max(n, 0)
+        lo, hi = c // m, (c + n) // m
+        for p in range(-(-lo // P), -(-hi // P)):
+            if p >= width:
+                missing += 1
+            elif free:
+                table[b, p] = free.pop()
+            else:
+                table[b, p] = -1
+                missing += 1
+        for i in range(lo, hi):
+            pg = table[b, i // P] if i // P < width else -1
+            req.append(b)
+            pos.append(i)
+            slot.append(int(pg) * P + i % P if pg >= 0 else -1)
+        start.append(len(req))
+    return table, start, req, pos, slot, missing, len(free)
+
+
+@pytest.mark.parametrize("B,m,P,maxc,maxn,short", [
+    (1, 1, 1, 0, 1, 0), (1, 1, 64, 1000, 1, 0), (5, 1, 16, 300, 40, 0), (33, 128, 16, 70000, 1500, 0),
+    (700, 1, 48, 500, 90, 0), (1500, 4, 64, 3000, 64, 0), (9, 1, 16, 200, 100, 7), (40, 4, 8, 900, 400, 1000)])
+def test_plan(B, m, P, maxc, maxn, short):
+    r = np.random.default_rng(B * 7 + m)
+    ctx = r.integers(0, maxc + 1, B)
+    new = np.where(r.random(B) < 0.3, 0, r.integers(0, maxn + 1, B))
+    new[0] = maxn
+    held = -(-(ctx // m) // P)
+    want = -(-((ctx + new) // m) // P)
+    width = max(1, int(want.max()) - (1 if short else 0))
+    table = np.full((B, width), -7, np.int32)
+    nid = 0
+    for b in range(B):
+        for p in range(min(int(held[b]), width)):
+            table[b, p] = nid
+            nid += 1
+    free = r.permutation(np.arange(nid, nid + int((want - held).sum()) + 3)).astype(np.int32)
+    n_free = max(0, len(free) - short)
+    total = int(((ctx + new) // m - ctx // m).sum())
+    plan = hca.PagePlan.empty(B, total + 5)
+    t, f = i32(table), i32(free)
+    got = hca.kv_page_plan(i32(ctx), i32(new), m, P, t, f, i32([n_free]), plan=plan)
+    rt, start, req, pos, slot, missing, left = plan_ref(ctx.tolist(), new.tolist(), m, P, table, free.tolist(), n_free)
+    assert got is plan
+    assert plan.row_start.tolist() == start
+    assert plan.row_req.tolist() == req + [-1] * 5
+    assert plan.row_pos.tolist() == pos + [-1] * 5
+    assert plan.slot.tolist() == slot + [-1] * 5
+    assert plan.missing.tolist() == [missing] and plan.free_left.tolist() == [left]
+    assert np.array_equal(t.cpu().numpy(), rt) and np.array_equal(f.cpu().numpy(), free)
+
+
+def test_plan_fewer_rows_than_items_negative_lengths_and_no_requests():
+    t = torch.full((3, 4), -1, dtype=torch.int32, device=DEV)
+    plan = hca.PagePlan.empty(3, 5)
+    hca.kv_page_plan(i32([-4, 3, 0]), i32([6, -2, 4]), 1, 4, t, i32([5, 6, 7, 8]), i32([99]), plan=plan)
+    assert plan.row_start.tolist() == [0, 6, 6, 10]
+    assert plan.slot.tolist() == [32, 33, 34, 35, 28] and plan.row_req.tolist() == [0] * 5
+    assert t.tolist() == [[8, 7, -1, -1], [-1] * 4, [6, -1, -1, -1]] and plan.free_left.tolist() == [1]
+    none = hca.kv_page_plan(i32([]), i32([]), 1, 4, torch.zeros((0, 2), dtype=torch.int32, device=DEV), i32([1, 2]),
+                            i32([2]), max_rows=3)
+    assert none.row_start.tolist() == [0] and none.free_left.tolist() == [2] and none.slot.tolist() == [-1] * 3
+
+
+# ------------------------------------------------------------------ stores
+@pytest.mark.parametrize("d", [128, 512])
+@pytest.mark.parametrize("extras", ["none", "norm", "rope", "both"])
+def test_store_bits(d, extras):
+    layout = LAYOUTS[d]
+    g = gen(d + len(extras))
+    n, P, pages = 37, 6, 11
+    x = bf((n + 2, d), g)
+    pos = torch.randint(0, 1 << 20, (n + 2,), generator=g, device=DEV).to(torch.int32)
+    slot = torch.randperm(P * pages, generator=g, device=DEV)[:n + 2]
+    slot[3], slot[8] = -1, P * pages
+    nw = 1.0 + 0.1 * torch.randn(d, generator=g, device=DEV) if extras in ("norm", "both") else None
+    fr = inp.rope_inv_freq(layout[1], device=DEV) if extras in ("rope", "both") else None
+    ee = None if extras == "none" else hca.EntryExtras(nw, 1e-6, fr)
+    plan = hca.PagePlan(i32([0, 20, n]), i32([0] * (n + 2)), pos, slot)
+    pool = torch.full((pages, P, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    assert hca.kv_page_store(x, plan, pool, layout, extras=ee) is pool
+    kw = {} if ee is None else dict(norm_w=None if nw is None else host(nw), eps=1e-6,
+                                    inv_freq=None if fr is None else host(fr))
+    want = host(torch.full((pages * P, d), 7.0, dtype=torch.bfloat16))
+    y = host(x) if ee is None else oracle.token_prep(host(x), pos.cpu().numpy(), layout[1], **kw)
+    for t in range(n):
+        s = int(slot[t])
+        if 0 <= s < pages * P:
+            want[s] = y[t]
+    assert np.array_equal(host(pool).reshape(-1, d), want)
+
+
+class Pool:
+    """Pages, block tables and free stack of one kind of item for B requests."""
+
+    def __init__(self, B, max_items, P, seed, spare=2):
+        self.P, self.width = P, max(1, -(-max_items // P))
+        n = B * self.width + spare
+        self.pages = n
+        self.table = torch.full((B, self.width), -1, dtype=torch.int32, device=DEV)
+        self.free = torch.randperm(n, generator=gen(seed), device=DEV).to(torch.int32)
+        self.count = i32([n])
+
+    def plan(self, ctx, new, m, max_rows):
+        p = hca.kv_page_plan(ctx, new, m, self.P, self.table, self.free, self.count, max_rows=max_rows)
+        self.count = p.free_left
+        return p
+
+    def rows(self, b, n):
+        t = self.table[b].cpu().numpy().astype(np.int64)
+        i = np.arange(n)
+        return t[i // self.P] * self.P + i % self.P
+
+
+@pytest.mark.parametrize("d,m,extras,P", [(128, 4, False, 5), (128, 128, True, 2), (512, 4, True, 16), (512, 128, False, 3),
+                                          (512, 128, True, 16)])
+def test_compress_bits_over_ragged_steps(d, m, extras, P):
+    """Random step lengths (none, one, many): every entry equals the oracle's
+    pooling of the whole sequence, whatever the steps cut its block into."""
+    layout = LAYOUTS[d]
+    g = gen(d + m)
+    B, T = 5, 700 if m == 128 else 90
+    x, gate = bf((B, T, d), g), bf((B, T, d), g)
+    bias = torch.randn((m, d), generator=g, device=DEV) * 0.5
+    nw = 1.0 + 0.1 * torch.randn(d, generator=g, device=DEV)
+    fr = inp.rope_inv_freq(layout[1], device=DEV)
+    ee = hca.EntryExtras(nw, 1e-6, fr) if extras else None
+    kw = dict(norm_w=host(nw), eps=1e-6, inv_freq=host(fr)) if extras else {}
+    rc, rs, rr = oracle.compress(host(x), host(gate), host(bias), m, T // m, layout[1], layout[2], **kw)[:3]
+    pool = Pool(B, T // m + 1, P, 1)
+    cache = hca.KVCache(pool.pages, P, layout, zero=True)
+    tx, tg = torch.zeros((B, m, d), dtype=torch.bfloat16, device=DEV), torch.zeros((B, m, d), dtype=torch.bfloat16, device=DEV)
+    r = np.random.default_rng(3)
+    ctx = np.zeros(B, np.int64)
+    for step in range(14):
+        top = {0: 1, 1: m, 2: 3 * m + 1}[step % 3]
+        new = np.minimum(np.where(r.random(B) < 0.2, 0, r.integers(0, top + 1, B)), T - ctx)
+        if new.sum() == 0:
+            continue
+        xs = torch.cat([x[b, ctx[b]:ctx[b] + new[b]] for b in range(B)])
+        gs = torch.cat([gate[b, ctx[b]:ctx[b] + new[b]] for b in range(B)])
+        starts = i32(np.concatenate([[0], np.cumsum(new)]))
+        plan = pool.plan(i32(ctx), i32(new), m, int(((ctx + new) // m - ctx // m).sum()) + 2)
+        hca.kv_page_compress(xs, gs, bias, starts, i32(ctx), plan, tx, tg, cache, extras=ee)
+        ctx = ctx + new
+        for b in range(B):
+            n = int(ctx[b]) % m
+            assert torch.equal(tx[b, :n], x[b, ctx[b] - n:ctx[b]]) and torch.equal(tg[b, :n], gate[b, ctx[b] - n:ctx[b]])
+    dn = layout[0] - layout[1]
+    for b in range(B):
+        k = int(ctx[b]) // m
+        at = pool.rows(b, k)
+        assert np.array_equal(host(cache.codes).reshape(-1, dn)[at], rc[b, :k])
+        assert np.array_equal(host(cache.scales).view(np.uint32).reshape(-1, dn // layout[2])[at], rs[b, :k].view(np.uint32))
+        assert np.array_equal(host(cache.rope).reshape(-1, layout[1])[at], rr[b, :k])
+    assert (ctx // m).sum() > B
+    untouched = np.ones(pool.pages * P, bool)
+    for b in range(B):
+        untouched[pool.rows(b, int(ctx[b]) // m)] = False
+    assert not host(cache.codes).reshape(-1, dn)[untouched].any()
+
+
+# ------------------------------------------------------------------ attention
+def entry_cache(pages, P, layout, g):
+    d, dr, grp = layout
+    y = torch.randn((pages, P, (d - dr) // grp, grp), generator=g, device=DEV) * 0.5
+    sc = y.abs().amax(-1) / 448.0
+    codes = (y / sc[..., None]).to(torch.float8_e4m3fn).view(torch.uint8).reshape(pages, P, d - dr)
+    return hca.KVCache.of(codes.contiguous(), sc.contiguous(), bf((pages, P, dr), g, 0.5))
+
+
+class Case:
+    def __init__(self, d, H, ctx, new, W, m=0, n_first=0, PE=16, PT=16, extras=False, seed=0, pad=3):
+        self.__dict__.update(d=d, H=H, ctx=list(ctx), new=list(new), W=W, m=m, n_first=n_first, extras=extras)
+        layout = self.layout = LAYOUTS[d]
+        g = gen(1000 + seed)
+        B, N = len(ctx), sum(new)
+        self.N, self.starts = N, np.concatenate([[0], np.cumsum(new)]).astype(np.int64)
+        end = [c + n for c, n in zip(ctx, new)]
+        self.PT, self.PE = PT, PE
+        self.tw = max(1, max(-(-e // PT) for e in end))
+        npt = B * self.tw + 1
+        self.ttab = torch.randperm(npt, generator=g, device=DEV)[:B * self.tw].view(B, self.tw).to(torch.int32).contiguous()
+        self.pages = bf((npt, PT, d), g)
+        self.cache = self.etab = None
+        if m:
+            self.ew = max(1, max(-(-(e // m) // PE) for e in end))
+            npe = B * self.ew + 1
+            self.etab = torch.randperm(npe, generator=g, device=DEV)[:B * self.ew].view(B, self.ew).to(torch.int32).contiguous()
+            self.cache = entry_cache(npe, PE, layout, g)
+        self.q = bf((N + pad, H, d), g)
+        self.scale = d ** -0.5
+        self.ex, self.kw, self.lens = None, {}, None
+        if extras:
+            nw, sink = 1.0 + 0.1 * torch.randn(d, generator=g, device=DEV), torch.randn(H, generator=g, device=DEV)
+            fr = inp.rope_inv_freq(layout[1], device=DEV)
+            self.ex = hca.AttnExtras(nw, 1e-6, sink, fr)
+            self.kw = dict(q_norm_w=host(nw), eps=1e-6, sink=host(sink), inv_freq=host(fr))
+
+    def run(self, max_new=None, out=None, ws=None, stream=None, q=None):
+        if self.lens is None or self.lens[0] != self.ctx:
+            # kept: a call on another stream still reads them after run() has returned
+            self.lens = (list(self.ctx), i32(self.starts), i32(self.ctx))
+            torch.cuda.synchronize()
+        a = (self.q if q is None else q, *self.lens[1:])
+        kw = dict(max_new=max_new, out=out, ws=ws, stream=stream, extras=self.ex)
+        if self.m:
+            return hca.paged_attn_chunk(*a, self.m, self.cache, self.etab, self.pages, self.ttab, self.W, self.scale, **kw)
+        return hca.paged_attn_window(*a, self.pages, self.ttab, self.W, self.n_first, self.scale, **kw)
+
+    def keys(self, b, p):
+        """(pool rows of the entries, pool rows of the tokens) that the query at position p of request b sees."""
+        ents, first, end = oracle.causal_keys(p, self.m, self.W)
+        toks = np.array(sorted(set(range(first, end)) | set(range(min(self.n_first, p + 1)))))
+        tt = self.ttab[b].cpu().numpy().astype(np.int64)
+        rows_t = tt[toks // self.PT] * self.PT + toks % self.PT
+        rows_e = np.zeros(0, np.int64)
+        if len(ents):
+            et = self.etab[b].cpu().numpy().astype(np.int64)
+            rows_e = et[ents // self.PE] * self.PE + ents % self.PE
+        return rows_e, rows_t
+
+    def pools(self):
+        d, dr, g = self.layout
+        if self.cache is None:
+            e = (np.zeros((1, d - dr), np.uint8), np.zeros((1, (d - dr) // g), np.float32), np.zeros((1, dr), np.uint16))
+        else:
+            e = (host(self.cache.codes).reshape(-1, d - dr), host(self.cache.scales).reshape(-1, (d - dr) // g),
+                 host(self.cache.rope).reshape(-1, dr))
+        return e, host(self.pages).reshape(-1, d)
+
+    def reference(self, rows=None):
+        """{row: (fp64 output [H][d], bound of the error)}"""
+        (c, s, r), toks = self.pools()
+        d, dr, g = self.layout
+        qh = host(self.q)
+        val = torch.from_numpy(np.arange(256, dtype=np.uint8)).view(torch.float8_e4m3fn).double().numpy()
+        out = {}
+        for b in range(len(self.ctx)):
+            for i in range(self.new[b]):
+                n = int(self.starts[b]) + i
+                if rows is not None and n not in rows:
+                    continue
+                p = self.ctx[b] + i
+                re, rt = self.keys(b, p)
+                o, _ = oracle.attend(qh[n], c, s, r, re, toks[rt], self.scale, g, q_pos=p, **self.kw)
+                # the bound: prepared query, keys in fp64, the softmax's own weights
+                q = oracle.bf16_to_f32(qh[n]).astype(np.float64)
+                if self.extras:
+                    q = q / np.sqrt((q * q).mean(-1, keepdims=True) + 1e-6) * self.kw["q_norm_w"]
+                    q[:, d - dr:] = np.stack([oracle.rope_f64(v, p, self.kw["inv_freq"]) for v in q[:, d - dr:]])
+                k = oracle.bf16_to_f32(toks[rt]).astype(np.float64)
+                if len(re):
+                    e = np.concatenate([val[c[re]] * np.repeat(s[re].astype(np.float64), g, 1),
+                                        oracle.bf16_to_f32(r[re]).astype(np.float64)], 1)
+                    k = np.concatenate([e, k])
+                lg = q @ k.T * self.scale
+                top = lg.max(1, keepdims=True)
+                if self.extras:
+                    top = np.maximum(top, self.kw["sink"][:, None])
+                w = np.exp(lg - top)
+                w /= w.sum(1, keepdims=True) + (np.exp(self.kw["sink"][:, None] - top) if self.extras else 0)
+                dl = self.scale * (np.abs(q) @ np.abs(k).T).max(1, keepdims=True) * (2 * U16 + 2.0 ** -14) + 2.0 ** -12
+                pv = w @ np.abs(k)
+                if self.extras:                          # the rotation back mixes a pair's errors
+                    pr = pv[:, d - dr:]
+                    pr[:, 0::2] = pr[:, 1::2] = pr[:, 0::2] + pr[:, 1::2]
+                out[n] = (o, (np.exp(2 * dl) - 1 + 4 * U16) * pv + UB * np.abs(o) + 1e-6)
+        return out
+
+    def check(self, got, rows=None):
+        ref = self.reference(rows)
+        g = f64(got)
+        num = den = 0.0
+        for n, (o, tol) in ref.items():
+            err = np.abs(g[n] - o)
+            assert np.all(err <= tol), (n, float((err - tol).max()), float(err.max()))
+            num += err.sum()
+            den += np.abs(o).sum()
+        assert num <= (1e-3 + 2.0 ** -9) * den, num / den
+
+
+CASES = [
+    # single tokens
+    dict(d=512, H=64, ctx=[1000, 5, 0, 4095], new=[1, 1, 1, 1], W=128, m=128),
+    dict(d=512, H=64, ctx=[30000], new=[1], W=128, m=4, PE=32),
+    dict(d=128, H=8, ctx=[1000, 127, 0, 64, 255], new=[1, 1, 1, 0, 1], W=128, m=128),
+    dict(d=128, H=1, ctx=[17, 300], new=[1, 1], W=7, n_first=3),
+    # chunks
+    dict(d=512, H=64, ctx=[0, 500, 127, 9], new=[5, 0, 3, 1], W=128, m=128, PE=1, PT=5),
+    dict(d=512, H=64, ctx=[2000, 383], new=[17, 2], W=100, m=128, extras=True),
+    dict(d=512, H=64, ctx=[2000, 0, 130], new=[3, 9, 6], W=128, n_first=4, extras=True),
+    dict(d=512, H=64, ctx=[77], new=[130], W=64, m=4, PE=48, PT=48),
+    dict(d=512, H=5, ctx=[600, 3], new=[30, 7], W=33, m=128, extras=True, PT=1),
+    dict(d=512, H=128, ctx=[300], new=[3], W=128, m=4),
+    dict(d=128, H=8, ctx=[1023, 0, 200], new=[40, 21, 1], W=128, m=128, extras=True),
+    dict(d=128, H=64, ctx=[90, 91], new=[2, 66], W=17, m=4, PE=7, PT=9),
+    dict(d=128, H=3, ctx=[500, 1, 60], new=[50, 3, 1], W=16, n_first=64, extras=True),
+    dict(d=128, H=16, ctx=[0], new=[1], W=1),
+    dict(d=512, H=64, ctx=[5, 0], new=[4, 70], W=1, n_first=1),
+    dict(d=512, H=64, ctx=[100, 4000], new=[70, 65], W=128, n_first=200),
+]
+
+
+@pytest.mark.parametrize("k", range(len(CASES)))
+def test_attention(k):
+    c = Case(seed=k, **CASES[k])
+    out = torch.full_like(c.q, 7.0)
+    got = c.run(out=out, max_new=max(c.new))
+    assert torch.all(got[c.N:] == 7.0)                   # rows behind the last request
+    c.check(got)
+
+
+@pytest.mark.parametrize("k", [4, 7, 12])
+def test_attention_without_the_bound(k):
+    """max_new only chooses kernels: none, too large and too small give results of the same tolerance."""
+    c = Case(seed=k, **CASES[k])
+    for mn in (None, 1, 10 ** 6):
+        c.check(c.run(max_new=mn))
+
+
+def test_attention_many_splits_and_long_offsets():
+    """One decode request over 20000 entries (every SM takes a split), pages far into a large pool."""
+    c = Case(512, 64, [20000 * 4 - 1], [1], 128, m=4, PE=64, PT=64)
+    c.check(c.run(max_new=1))
+
+
+def test_token_rows_beyond_32_bits():
+    """A pool of more than 2^32 elements: the last pages are the request's."""
+    c = Case(512, 64, [200], [3], 128, n_first=4, PT=64)
+    n = (1 << 32) // (64 * 512) + 8
+    big = torch.empty((n, 64, 512), dtype=torch.bfloat16, device=DEV)
+    last = torch.arange(n - c.pages.shape[0], n, device=DEV)
+    big[last] = c.pages
+    small, table = c.pages, c.ttab
+    c.pages, c.ttab = big, (table + (n - small.shape[0])).to(torch.int32)
+    got = c.run()
+    c.pages, c.ttab = small, table
+    c.check(got)
+
+
+def test_unused_page_rows_may_hold_anything():
+    """NaN, infinities and garbage everywhere but in the visible keys' rows change nothing."""
+    for k in (0, 4, 6, 12):
+        c = Case(seed=k, **CASES[k])
+        clean = c.run()
+        used_t, used_e = set(), set()
+        for b in range(len(c.ctx)):
+            for i in range(c.new[b]):
+                re, rt = c.keys(b, c.ctx[b] + i)
+                used_t |= set(rt.tolist())
+                used_e |= set(re.tolist())
+        free_t = [r for r in range(c.pages.shape[0] * c.PT) if r not in used_t]
+        c.pages.view(-1, c.d)[free_t] = float("nan")
+        if c.cache is not None:
+            free_e = [r for r in range(c.cache.B * c.PE) if r not in used_e]
+            c.cache.codes.view(-1, c.cache.codes.shape[2])[free_e] = 0x7F
+            c.cache.scales.view(-1, c.cache.scales.shape[2])[free_e] = float("inf")
+            c.cache.rope.view(-1, c.cache.rope.shape[2])[free_e] = float("-inf")
+        assert torch.equal(c.run()[:c.N], clean[:c.N])
+
+
+@pytest.mark.parametrize("d,H", [(512, 64), (128, 8)])
+def test_non_finite_key_reaches_only_the_queries_that_see_it(d, H):
+    c = Case(d, H, [300], [12], 20, m=4, PT=8)
+    clean = c.run()
+    p_bad = 306                                          # a token of the step itself
+    row = int(c.ttab[0, p_bad // 8]) * 8 + p_bad % 8
+    c.pages.view(-1, d)[row, 3] = float("inf")
+    e_bad = 76                                           # visible from position 307 on
+    er = int(c.etab[0, e_bad // 16]) * 16 + e_bad % 16
+    c.cache.codes.view(-1, c.cache.codes.shape[2])[er, 5] = 0x7F
+    got = c.run()
+    for i in range(12):
+        if 300 + i >= p_bad:
+            assert torch.isnan(got[i]).all()
+        else:
+            assert torch.equal(got[i], clean[i])
+
+
+def test_pages_outside_the_pool_are_not_visible():
+    c = Case(512, 64, [100, 40, 900], [2, 3, 2], 32, m=4, PT=16, PE=4)
+    ref = Case(512, 64, [100, 40, 900], [2, 3, 2], 32, m=4, PT=16, PE=4)
+    c.etab[0, 3], c.etab[2, 0] = -1, c.cache.B           # entries 12..15 of request 0, 0..3 of request 2
+    c.ttab[1, :] = c.pages.shape[0] + 5                  # request 1 has no token at all ...
+    c.etab[1, :] = -(1 << 31)                            # ... and no entry: nothing is visible
+    got = c.run()
+    keys = ref.keys
+
+    def without(b, p):
+        re, rt = keys(b, p)
+        if b == 0:
+            re = np.delete(re, np.arange(12, 16))
+        if b == 2:
+            re = re[4:]
+        return re, rt
+    ref.keys = without
+    ref.check(got, rows=[0, 1, 5, 6])
+    assert torch.all(got[2:5] == 0)
+
+
+def test_sink_without_keys_and_large_sinks():
+    c = Case(128, 8, [10], [2], 8, m=4, extras=True)
+    c.ttab[:] = -1
+    c.etab[:] = -1
+    assert torch.all(c.run()[:2] == 0)
+    c = Case(512, 64, [10], [3], 8, m=4, extras=True)
+    c.ex.sink[:] = 80.0
+    assert torch.all(c.run()[:3].abs() < 1e-20)
+
+
+def test_queries_of_zero_give_the_mean():
+    c = Case(512, 64, [700], [4], 128, m=128)
+    c.q.zero_()
+    c.check(c.run())
+
+
+def test_streams_graphs_and_two_calls_at_once():
+    c = Case(seed=4, **CASES[4])
+    e = Case(seed=1, **CASES[1])
+    want, wante = c.run(max_new=5), e.run(max_new=1)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(10):
+        a, b = c.run(max_new=5, stream=s1), e.run(max_new=1, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a[:c.N], want[:c.N]) and torch.equal(b[:e.N], wante[:e.N])
+    # two captured steps, each with its own buffers, replayed side by side; new lengths between replays
+    cap = torch.cuda.Stream()
+    cap.wait_stream(torch.cuda.current_stream())
+    starts, ctx = i32(c.starts), i32(c.ctx)
+    out, oute = torch.zeros_like(c.q), torch.zeros_like(e.q)
+    st_e, ctx_e = i32(e.starts), i32(e.ctx)
+    with torch.cuda.stream(cap):
+        g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g1, stream=cap):
+            hca.paged_attn_chunk(c.q, starts, ctx, c.m, c.cache, c.etab, c.pages, c.ttab, c.W, c.scale, max_new=5, out=out)
+        with torch.cuda.graph(g2, stream=cap):
+            hca.paged_attn_chunk(e.q, st_e, ctx_e, e.m, e.cache, e.etab, e.pages, e.ttab, e.W, e.scale, max_new=1, out=oute)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        out.zero_(), oute.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s1):
+            g1.replay()
+        with torch.cuda.stream(s2):
+            g2.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[:c.N], want[:c.N]) and torch.equal(oute[:e.N], wante[:e.N])
+    ctx_e.fill_(29000)
+    g2.replay()
+    torch.cuda.synchronize()
+    e.ctx = [29000]
+    assert torch.equal(oute[:1], e.run(max_new=1)[:1])
+
+
+def test_same_call_same_bytes():
+    for k in (1, 5, 7):
+        c = Case(seed=k, **CASES[k])
+        a = c.run()
+        assert all(torch.equal(a[:c.N], c.run()[:c.N]) for _ in range(3))
+
+
+def test_refusals_of_the_binding():
+    c = Case(128, 8, [10], [2], 8, m=4)
+    with pytest.raises(TypeError):
+        c.run(q=c.q.float())
+    with pytest.raises(ValueError):
+        c.run(q=c.q.transpose(0, 1))
+    with pytest.raises(ValueError):
+        c.run(out=c.q[:1])
+    with pytest.raises(ValueError):
+        hca.paged_attn_window(c.q.cpu(), i32(c.starts), i32(c.ctx), c.pages, c.ttab, 8, 0, c.scale)
+    with pytest.raises(ValueError):
+        hca.paged_attn_window(c.q, i32(c.starts)[:-1], i32(c.ctx), c.pages, c.ttab, 8, 0, c.scale)
+    for W, first, scale in ((0, 0, 1.0), (5000, 0, 1.0), (8, -1, 1.0), (8, 0, 0.0), (8, 0, float("nan"))):
+        with pytest.raises(hca.HCAError):
+            hca.paged_attn_window(c.q, i32(c.starts), i32(c.ctx), c.pages, c.ttab, W, first, scale)
+    big = Case(512, 64, [30000], [1], 128, m=4)
+    assert hca.paged_attn_workspace_size(big.q.shape[0], 1, 64, big.layout, 1, big.ew * 16, 128) > 16
+    with pytest.raises(hca.HCAError):
+        big.run(max_new=1, ws=torch.empty(16, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        hca.KVCache.of(big.cache.codes, big.cache.scales[:, :, :3].contiguous(), big.cache.rope)
+    with pytest.raises(ValueError):
+        hca.kv_page_plan(i32([1]), i32([1]), 1, 4, i32([[0]]), i32([1]), i32([1]))
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("d,H,section9", [(128, 8, False), (128, 8, True), (512, 64, True)])
+def test_steps_of_a_ragged_batch(d, H, section9):
+    """Requests join, prefill in chunks, decode and idle together over a window
+    layer (ratio 0, first tokens visible) and an HCA layer (ratio 128): plan,
+    store, compress and attention of every step against the oracle's own
+    pooling and attention over the whole sequences."""
+    from long_context_attention_hca_b200.pipeline import PagedLoop
+    layout = LAYOUTS[d]
+    dr, grp = layout[1], layout[2]
+    W, first, B, T, m = 64, 3, 4, 420, 128
+    g = gen(900 + d + section9)
+    ratios = [0, m]
+    x = [bf((B, T, d), g) for _ in ratios]
+    gate = [bf((B, T, d), g) for _ in ratios]
+    bias = torch.randn((m, d), generator=g, device=DEV) * 0.5
+    s9 = None
+    if section9:
+        s9 = [{"kv_norm_w": 1.0 + 0.1 * torch.randn((d,), generator=g, device=DEV),
+               "q_norm_w": 1.0 + 0.1 * torch.randn((d,), generator=g, device=DEV),
+               "sink": torch.randn((H,), generator=g, device=DEV),
+               "inv_freq": inp.rope_inv_freq(dr, device=DEV), "eps": 1e-6} for _ in ratios]
+    loop = PagedLoop(B, H, layout, ratios, W, first, max_tokens=T, max_rows=260, softmax_scale=d ** -0.5,
+                     token_page=16, entry_page=2, s9=s9)
+    loop.set_bias(1, bias)
+    kw = {} if not section9 else dict(norm_w=host(s9[1]["kv_norm_w"]), eps=1e-6, inv_freq=host(s9[1]["inv_freq"]))
+    ent = oracle.compress(host(x[1]), host(gate[1]), host(bias), m, T // m, dr, grp, **kw)[:3]
+    steps = [[130, 0, 3, 0], [1, 0, 1, 60], [127, 40, 1, 1], [1, 1, 0, 1], [0, 88, 90, 67], [60, 1, 33, 1], [1, 1, 1, 0]]
+    ctx = np.zeros(B, np.int64)
+    for new in steps:
+        new = np.array(new)
+        N = int(new.sum())
+        cat = lambda t: torch.cat([t[b, ctx[b]:ctx[b] + new[b]] for b in range(B)])
+        q = [bf((N, H, d), g) for _ in ratios]
+        out = loop.step(i32(new), [cat(t) for t in x], [cat(t) for t in gate], q, max_new=int(new.max()))
+        torch.cuda.synchronize()
+        starts = np.concatenate([[0], np.cumsum(new)])
+        for li, r in enumerate(ratios):
+            for b in range(B):
+                for i in range(int(new[b])):
+                    if i % 11 and i != new[b] - 1:
+                        continue
+                    p = int(ctx[b] + i)
+                    ents, w0, w1 = oracle.causal_keys(p, r, W)
+                    tk = sorted(set(range(w0, w1)) | (set(range(min(first, p + 1))) if r == 0 else set()))
+                    win = host(x[li])[b, tk]
+                    akw = {}
+                    if section9:
+                        P = s9[li]
+                        win = oracle.token_prep(win, np.array(tk), dr, norm_w=host(P["kv_norm_w"]), eps=1e-6,
+                                                inv_freq=host(P["inv_freq"]))
+                        akw = dict(q_norm_w=host(P["q_norm_w"]), eps=1e-6, sink=host(P["sink"]),
+                                   inv_freq=host(P["inv_freq"]), q_pos=p)
+                    n = int(starts[b]) + i
+                    e = [a[b] for a in ent]
+                    ref, _ = oracle.attend(host(q[li])[n], *e, ents, win, d ** -0.5, grp, **akw)
+                    err = np.abs(f64(out[li])[n] - ref)
+                    assert err.max() <= 1e-2 + UB * np.abs(ref).max(), (li, b, p, err.max())
+                    assert err.sum() <= (1e-3 + 2.0 ** -9) * np.abs(ref).sum() + 1e-4 * ref.size, (li, b, p)
+        ctx += new
+        assert loop.ctx.tolist() == ctx.tolist() and loop.missing() == 0
+
+
+def test_released_requests_give_their_pages_back():
+    from long_context_attention_hca_b200.pipeline import PagedLoop
+    d, H, B, T = 128, 8, 2, 300
+    g = gen(31)
+    x, gate = bf((T, d), g), bf((T, d), g)
+    bias = torch.randn((128, d), generator=g, device=DEV) * 0.5
+    q = bf((T, H, d), g)
+    loop = PagedLoop(B, H, LAYOUTS[d], [128], 32, 0, max_tokens=T, max_rows=T, softmax_scale=d ** -0.5, token_page=16,
+                     entry_page=1, token_pages=20, entry_pages=2)
+    loop.set_bias(0, bias)
+    outs = []
+    for who in ([T, 0], [0, T], [T, 0]):
+        outs.append(loop.step(i32(who), [x], [gate], [q])[0])
+        assert loop.missing() == 0
+        loop.release(0 if who[0] else 1)
+        assert loop.n_free_tokens.item() == 20 and loop.n_free_entries.item() == 2
+        assert sorted(loop.free_tokens.tolist()) == list(range(20))
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    loop.step(i32([T, T]), [torch.cat([x, x])[:T]], [torch.cat([gate, gate])[:T]], [q])
+    assert loop.missing() > 0                            # two requests do not fit: reported, not written elsewhere
