@@ -49,6 +49,7 @@ int attn_prefill_launch(const uint16_t* q, int Tq, int H, int p0, int m, const h
 
 int tc_take_device_error();
 int index_take_device_error();
+int paged_take_device_error();
 
 static thread_local int g_last_cuda_error = 0;
 void set_last_cuda_error(int e) { g_last_cuda_error = e; }
@@ -166,8 +167,8 @@ int hca_set_early_query(int on) {
 }
 
 int hca_take_device_error(void) {
-    const int a = tc_take_device_error(), b = index_take_device_error();
-    return (a < 0 || b < 0) ? -1 : (a | b);
+    const int a = tc_take_device_error(), b = index_take_device_error(), c = paged_take_device_error();
+    return (a < 0 || b < 0 || c < 0) ? -1 : (a | b | c);
 }
 
 int csa_compress(const uint16_t* x, const uint16_t* gate, int64_t x_seq_stride, const float* pos_bias,

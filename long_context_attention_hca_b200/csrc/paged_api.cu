@@ -18,8 +18,8 @@ int page_compress_launch(int m, const uint16_t* x, const uint16_t* gate, int64_t
                          const int32_t* ent_pos, const int64_t* ent_slot, int64_t max_ent, uint16_t* tail_x,
                          uint16_t* tail_gate, const hca_kv_layout& L, const hca_kv_cache& pool, int64_t n_slots,
                          const hca_entry_extras* ex, cudaStream_t st);
-size_t paged_attn_ws_bytes(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_keys);
-int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_keys, void* ws, size_t ws_bytes,
+size_t paged_attn_ws_bytes(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_entries, int W, int n_first);
+int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_entries, void* ws, size_t ws_bytes,
                       cudaStream_t st);
 
 namespace {
@@ -43,9 +43,6 @@ bool entry_extras_ok(const hca_entry_extras* ex) {
 bool map_ok(const hca_page_map& m) {
     return m.page_size >= 1 && m.width >= 0 && m.pages >= 0 && (m.width == 0 || (m.table && (reinterpret_cast<uintptr_t>(m.table) & 3u) == 0));
 }
-
-// the longest key list of a tile: entries, first tokens, the window and the tile's own tokens
-int64_t key_bound(int64_t max_entries, int32_t W, int32_t n_first) { return max_entries + W + n_first + 64; }
 
 int attn_common(const uint16_t* q, int64_t n_rows, int32_t H, int32_t B, const int32_t* row_start,
                 const int32_t* ctx_len, int64_t max_new, int32_t m, const hca_kv_layout& L, const hca_kv_cache* pool,
@@ -81,8 +78,8 @@ int attn_common(const uint16_t* q, int64_t n_rows, int32_t H, int32_t B, const i
     p.scale_log2 = scale * paged::LOG2E;
     p.out = out;
     const int64_t max_entries = pool ? static_cast<int64_t>(emap->width) * emap->page_size : 0;
-    return paged_attn_launch(p, L.d, max_new > 0 && max_new < n_rows ? max_new : n_rows, key_bound(max_entries, W, n_first),
-                             ws, ws_bytes, as_stream(stream));
+    return paged_attn_launch(p, L.d, max_new > 0 && max_new < n_rows ? max_new : n_rows, max_entries, ws, ws_bytes,
+                             as_stream(stream));
 }
 
 }  // namespace
@@ -144,8 +141,8 @@ size_t paged_attn_workspace_size(int64_t n_rows, int32_t B, int32_t H, hca_kv_la
     if (n_rows <= 0 || B <= 0 || !layout_ok(layout) || H < 1 || H > 128 || max_new < 0 || max_entries < 0 || W < 1 ||
         W > 4096 || n_first < 0 || n_first > 4096 || n_rows * H > 0x7FFFFFFFLL - 0x10000)
         return 0;
-    return paged_attn_ws_bytes(n_rows, B, H, layout.d, max_new > 0 && max_new < n_rows ? max_new : n_rows,
-                               key_bound(max_entries, W, n_first));
+    return paged_attn_ws_bytes(n_rows, B, H, layout.d, max_new > 0 && max_new < n_rows ? max_new : n_rows, max_entries, W,
+                               n_first);
 }
 
 int paged_attn_chunk(const uint16_t* q, int64_t n_rows, int32_t H, int32_t B, const int32_t* row_start,

@@ -16,6 +16,10 @@
 namespace hca {
 namespace paged {
 
+int64_t tc_stage_rows(int64_t n_rows, int B, int64_t max_entries, int W, int n_first);
+size_t tc_stage_bytes(int64_t rows);
+int tc_chunk_launch(const Params& p, int64_t max_entries, void* ws, cudaStream_t st);
+
 // ---------------------------------------------------------------- row kernel
 // One CTA = one tile of R rows (tokens x heads, flattened inside a request) and
 // one split of its keys.  8 warps: R / 16 row groups x KG key groups; warp
@@ -457,6 +461,12 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
 }
 
 // ---------------------------------------------------------------- host side
+// A request goes to the chunk kernel when its rows fill two CTA pairs.
+constexpr int CHUNK_ROWS = 256;
+// Staged keys take 1 KB each: at most 2 GB of workspace, beyond that (64
+// requests whose tables reach 4M tokens, say) every request is the row kernel's.
+constexpr int64_t MAX_STAGE_ROWS = 2ll << 20;
+
 // Rows of a tile: 16 when no request can fill more (a small head count at
 // decode), else 64.
 inline int tile_rows(int64_t max_new, int H) { return max_new * H <= 16 ? 16 : 64; }
@@ -472,17 +482,36 @@ inline int split_count(int64_t tiles, int64_t max_keys) {
     return s < 1 ? 1 : static_cast<int>(s);
 }
 
-struct Plan { int R, splits; int64_t tiles; };
+// chunk: requests with at least this many new tokens go to the chunk kernel
+// (0: none do), the others to the row kernel, tiles_per_req tiles each.
+struct Plan { int R, splits, tiles_per_req, chunk; int64_t tiles; size_t stage_bytes; };
 
-static Plan make_plan(int64_t n_rows, int B, int H, int64_t max_new, int64_t max_keys) {
-    Plan k;
-    // n_rows rows over B requests: a tile for each request at least, whatever the lengths
+static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_entries, int W, int n_first) {
+    Plan k = {};
+    // the longest key list of a tile: entries, first tokens, the window and the tile's own tokens
+    const int64_t max_keys = max_entries + W + n_first + 64;
+    const int64_t stage_rows = tc_stage_rows(n_rows, B, max_entries, W, n_first);
+    const int chunk = (CHUNK_ROWS + H - 1) / H < 2 ? 2 : (CHUNK_ROWS + H - 1) / H;
+    const int64_t reqs = n_rows < B ? n_rows : B;      // requests that can have a new token
+    if (D == 512 && max_new >= chunk && stage_rows <= MAX_STAGE_ROWS) {
+        k.chunk = chunk;
+        k.stage_bytes = tc_stage_bytes(stage_rows);
+        k.R = 64;
+        k.tiles_per_req = (static_cast<int64_t>(chunk - 1) * H + k.R - 1) / k.R;
+        k.tiles = static_cast<int64_t>(B) * k.tiles_per_req;
+        k.splits = split_count(reqs, max_keys);
+        return k;
+    }
     k.R = tile_rows(max_new, H);
     k.tiles = tile_count(n_rows, H, B, k.R);
-    // tiles that can hold rows: every request's rows, rounded up
-    const int64_t busy = n_rows * H / k.R + (n_rows < B ? n_rows : B);
-    k.splits = split_count(n_rows * H <= static_cast<int64_t>(B) * k.R ? (n_rows < B ? n_rows : B) : busy, max_keys);
+    // tiles that can hold rows: one a request when no request fills more
+    k.splits = split_count(max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs, max_keys);
     return k;
+}
+
+static size_t part_bytes(const Plan& k, int D) {
+    if (k.splits <= 1) return 0;
+    return static_cast<size_t>(k.tiles) * k.splits * k.R * (static_cast<size_t>(D) * 2 + 2 * sizeof(float)) + 256;
 }
 
 template <int D, int R>
@@ -503,21 +532,26 @@ static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
 
 }  // namespace paged
 
-size_t paged_attn_ws_bytes(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_keys) {
-    const paged::Plan k = paged::make_plan(n_rows, B, H, max_new, max_keys);
-    if (k.splits <= 1) return 0;
-    return static_cast<size_t>(k.tiles) * k.splits * k.R * (static_cast<size_t>(D) * 2 + 2 * sizeof(float)) + 256;
+size_t paged_attn_ws_bytes(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_entries, int W, int n_first) {
+    const paged::Plan k = paged::make_plan(n_rows, B, H, D, max_new, max_entries, W, n_first);
+    return k.stage_bytes + paged::part_bytes(k, D);
 }
 
-int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_keys, void* ws, size_t ws_bytes,
+int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_entries, void* ws, size_t ws_bytes,
                       cudaStream_t st) {
-    const paged::Plan k = paged::make_plan(p.n_rows, p.B, p.H, max_new, max_keys);
+    const paged::Plan k = paged::make_plan(p.n_rows, p.B, p.H, D, max_new, max_entries, p.W, p.n_first);
+    const size_t need = k.stage_bytes + paged::part_bytes(k, D);
+    if (need > 0 && (ws == nullptr || ws_bytes < need)) return HCA_ERR_WORKSPACE;
     p.n_splits = k.splits;
     p.min_chunk = 0x7FFFFFFF;
+    if (k.chunk > 0) {
+        p.min_chunk = k.chunk;
+        const int rc = paged::tc_chunk_launch(p, max_entries, ws, st);
+        if (rc != HCA_OK) return rc;
+        p.tiles_per_req = k.tiles_per_req;
+    }
     if (k.splits > 1) {
-        if (ws == nullptr || ws_bytes < paged_attn_ws_bytes(p.n_rows, p.B, p.H, D, max_new, max_keys))
-            return HCA_ERR_WORKSPACE;
-        p.part_o = static_cast<uint16_t*>(ws);
+        p.part_o = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + k.stage_bytes);
         p.part_ml = reinterpret_cast<float*>(p.part_o + static_cast<size_t>(k.tiles) * k.splits * k.R * D);
     }
     if (D == 512)

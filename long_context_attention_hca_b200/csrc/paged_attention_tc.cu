@@ -1,0 +1,713 @@
+// paged_attention_tc.cu -- attention of prefill chunks over paged caches on the
+// sm_100a tensor cores, d = 512 (paged_attention.cu holds the attention rule
+// and the kernel for few rows).
+//
+// Two kernels.  The first writes each chunk request's keys once, dequantised to
+// fp16, into rows of the workspace (entries, then first tokens and window
+// tokens in position order): every one of the request's tokens reads them, so
+// that a page lookup, a dequantisation and a check for non-finite values per
+// key is paid once and the second kernel is fed by TMA alone.
+//
+// The second runs on CTA pairs (cta_group::2): 128 rows (tokens x heads,
+// flattened), 64 in each CTA, against tiles of 128 keys.
+//   S = Q K^T    M = 128, N = 128, K = 512: each CTA holds its 64 rows of Q and
+//                64 of the tile's keys
+//   O += P V     M = 128, N = 2 x 256, K = 128: each CTA holds its 64 rows of P
+//                and half of the dims of all 128 keys
+// Why pairs: a CTA's O is 64 rows x 512 dims of fp32, half of its TMEM, and an
+// M = 128 instruction over two CTAs keeps the tensor pipe at its full rate
+// where M = 64 in one CTA runs at half; and each CTA reads half of B.
+// TMEM (every row on two lanes: lane r holds the first half of an
+// instruction's N, lane 64 + r the second): S in 2 buffers of 64 columns, O in
+// 2 x 128 columns.
+//
+// Per 128-key tile and CTA: 48 instructions, 2048 clocks at the tensor pipe's
+// rate; shared memory moves 256 KB for QK's operands (1024 clocks at 128 B), 96
+// KB for PV's (768) and 128 KB in.  The K and V parts of a tile are separate
+// 16 KB pieces of one ring of 8, consumed in the order QK(0), QK(i + 1), PV(i),
+// ...: the softmax of tile i runs beside QK(i + 1).
+//
+// Warps: 0-7 softmax and output (a row is shared by 4 threads: 2 TMEM lanes x 2
+// column halves), 8 TMA, 9 QK issue, 10 PV issue (the first CTA's only).
+// The online softmax is in base 2; O is rescaled only when a row's maximum
+// grows by more than 2^8 (P <= 2^8 in fp16).  Every wait is bounded: one that
+// gives up sets the device error word, the CTA's outputs become NaN, and the
+// pair still meets at the end.
+#include <cuda.h>
+
+#include "paged_attention.cuh"
+
+namespace hca {
+
+__device__ int g_paged_device_error = 0;
+
+namespace paged {
+namespace tcp {
+
+constexpr int D = 512;
+constexpr int PAIR = 128;                    // rows of a CTA pair
+constexpr int ROWS = 64;                     // rows of one CTA
+constexpr int HALF = 64;                     // keys of a half tile (one CTA's K)
+constexpr int NSLOT = 8, SLOT = 16384;
+constexpr int Q_OFF = 0;                     // 8 column blocks (64 dims) of 64 rows x 128 B
+constexpr int P_OFF = 65536;                 // 2 column blocks (64 keys) of 64 rows x 128 B
+constexpr int R_OFF = P_OFF + 16384;
+constexpr int SMEM = R_OFF + NSLOT * SLOT + 1024;
+constexpr int NSOFT = 8, NTHREADS = 11 * 32;
+constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 512;
+constexpr float GROW = 8.0f;                 // log2 units
+constexpr int DR = 64, DN = D - DR;
+constexpr long long WAIT_CLOCKS = 2000000000ll;   // about a second
+
+struct Stage {
+    uint16_t* rows;             // [bound][512] fp16
+    uint8_t* flags;             // [bound]: 1 not visible, 2 non-finite
+    int64_t per_req;            // rows of a request besides its new tokens
+    int64_t bound;              // rows of the workspace
+};
+
+// Request b's staged rows start at b per_req + row_start[b]: entries (padded
+// with zeros to a multiple of 64), first tokens [0, f), tokens from w0 on, and
+// 64 rows of zeros (a half tile may reach past its last key; V must be finite).
+struct Region {
+    int64_t base, w0;
+    int n_e, n_e64, f;
+};
+
+__device__ __forceinline__ Region region(const Params& p, const Stage& s, int b, int64_t ctx, int n_new) {
+    Region r;
+    r.base = b * s.per_req + p.row_start[b];
+    r.n_e = static_cast<int>(entries_before(p, ctx + n_new - 1));
+    r.n_e64 = (r.n_e + 63) & ~63;
+    r.w0 = ctx - (p.W - 1) > 0 ? ctx - (p.W - 1) : 0;
+    r.f = static_cast<int>(p.n_first < r.w0 ? p.n_first : r.w0);
+    return r;
+}
+
+// ------------------------------------------------------------------ staging
+// A warp per staged row, 16 dims a lane.  Bound: DRAM and L2 (604 or 1024 B in,
+// 1 KB out a row).
+__global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
+    const int lane = threadIdx.x & 31;
+    const int64_t g = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    pdl_trigger();                              // the attention's prologue may start
+    if (g >= s.bound) return;
+    // largest b with b per_req + row_start[b] <= g
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+        const int step = (hi - lo + 31) / 32;
+        const int c = lo + lane * step;
+        const bool le = c < hi && (c == lo || c * s.per_req + p.row_start[c] <= g);
+        const unsigned mask = __ballot_sync(0xffffffffu, le);
+        lo += (31 - __clz(mask)) * step;
+        if (lo + step < hi) hi = lo + step;
+    }
+    const int b = lo;
+    const int64_t st = p.row_start[b];
+    const int64_t en = p.row_start[b + 1] < p.n_rows ? p.row_start[b + 1] : p.n_rows;
+    const int n_new = st < 0 || en < st ? 0 : static_cast<int>(en - st);
+    if (n_new < p.min_chunk) return;
+    const int64_t ctx = p.ctx[b] > 0 ? p.ctx[b] : 0;
+    const Region r = region(p, s, b, ctx, n_new);
+    int64_t i = g - r.base;
+    if (i < 0) return;
+    uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    int64_t row = -1;
+    const int d0 = lane * 16;
+    if (i < r.n_e64) {
+        if (i < r.n_e) row = entry_row(p, b, static_cast<uint32_t>(i));
+        if (row >= 0) {
+            if (d0 < DN) {
+                const uint4 cv = __ldg(reinterpret_cast<const uint4*>(p.codes + row * DN + d0));
+                const float sc = __ldg(p.scales + row * (DN / 64) + d0 / 64);
+                const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[k] & 0xFFFFu)));
+                    const float2 c = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[k] >> 16)));
+                    h[2 * k] = pack_half2(a.x * sc, a.y * sc);
+                    h[2 * k + 1] = pack_half2(c.x * sc, c.y * sc);
+                }
+            } else {
+                const uint4* rp = reinterpret_cast<const uint4*>(p.rope + row * DR + (d0 - DN));
+                const uint4 a = __ldg(rp), c = __ldg(rp + 1);
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    h[k] = pack_half2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+            }
+        }
+    } else {
+        i -= r.n_e64;
+        const int64_t n_t = ctx + n_new - r.w0;
+        if (i >= r.f + n_t + HALF) return;
+        if (i < r.f + n_t) row = token_row(p, b, static_cast<uint32_t>(i < r.f ? i : r.w0 + (i - r.f)));
+        if (row >= 0) {
+            const uint4* rp = reinterpret_cast<const uint4*>(p.tok + row * D + d0);
+            const uint4 a = __ldg(rp), c = __ldg(rp + 1);
+            const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                h[k] = pack_half2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+        }
+    }
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) bad = bad || bad_half2(h[k]);
+    bad = __any_sync(0xffffffffu, bad);
+    const uint32_t keep = bad ? 0u : 0xffffffffu;
+    uint4* dst = reinterpret_cast<uint4*>(s.rows + g * D + d0);
+    dst[0] = make_uint4(h[0] & keep, h[1] & keep, h[2] & keep, h[3] & keep);
+    dst[1] = make_uint4(h[4] & keep, h[5] & keep, h[6] & keep, h[7] & keep);
+    if (lane == 0) s.flags[g] = row < 0 ? 1 : (bad ? 2 : 0);
+}
+
+// ------------------------------------------------------------------ PTX
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ uint32_t cta_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t in_first(uint32_t addr) {     // the same address in the pair's first CTA
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" :: "r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+// a tile of the staged rows into this CTA, its bytes counted at the barrier of the pair's first CTA
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar_first) {
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar_first) : "memory");
+}
+__device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc) : "memory");
+}
+// arrives at `bar` of both CTAs once this thread's MMAs so far have completed
+__device__ __forceinline__ void commit2(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+                 :: "r"(bar), "h"(static_cast<uint16_t>(3)) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+                   "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
+                   "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+                   "=r"(r[30]), "=r"(r[31])
+                 : "r"(a));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 :: "r"(a), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                    "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+                    "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+// shared-memory matrix descriptor, 128-byte swizzle (sm_100 format)
+__device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+           (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (1ull << 46) | (2ull << 61);
+}
+// instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator
+constexpr uint32_t idesc_f16(int M, int N, int b_mn) {
+    return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+           (static_cast<uint32_t>(M >> 4) << 24);
+}
+// byte offset of (row, 16-byte chunk c in 0..7) inside a column block of 128-byte rows (128-byte swizzle)
+__device__ __forceinline__ uint32_t sw128(int row, int c) {
+    return static_cast<uint32_t>((row >> 3) * 1024 + (row & 7) * 128 + ((c ^ (row & 7)) << 4));
+}
+
+// Bounded wait of a whole warp, the same answer for all its lanes.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+    bool done = mbar_try(bar, parity);
+    if (!__all_sync(0xffffffffu, done)) {
+        const long long t0 = clock64();
+        while (!done && !*abort_flag && clock64() - t0 < WAIT_CLOCKS) done = mbar_try(bar, parity);
+        if (!__all_sync(0xffffffffu, done)) {
+            *abort_flag = 1;
+            atomicExch(&g_paged_device_error, 1);
+            return false;
+        }
+    }
+    return true;
+}
+
+// ring position of piece 0 of K(i) and V(i): K(0), then K(i + 1), V(i) in turn
+__device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 8 * i - 4; }
+__device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 8 * i + 4 : 8 * i + 8; }
+
+struct Ctrl {
+    uint64_t full[NSLOT], empty[NSLOT], s_full[2], p_full[2], pv_done, drain;
+    float mx[2][4][ROWS];
+    float l[4][ROWS];
+    uint32_t tmem;
+    int abort_flag;
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
+paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) Ctrl c;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t rank = cta_rank();
+    const uint32_t sbase = smem_u32(smem);
+    volatile int* abort_flag = &c.abort_flag;
+
+    Tile T;
+    if (!make_tile(p, blockIdx.x >> 1, PAIR, T) || T.n_new < p.min_chunk) return;   // both CTAs alike
+    const Region rg = region(p, s, T.b, T.ctx, T.n_new);
+    // half tiles of 64 staged rows: entries, first tokens, window
+    const int h_e = (T.n_e + HALF - 1) / HALF, h_f = (T.n_f + HALF - 1) / HALF, h_w = (T.n_w + HALF - 1) / HALF;
+    const int n_half = h_e + h_f + h_w;
+    const int n = (n_half + 1) / 2;
+    const int64_t tok0 = rg.base + rg.n_e64;
+    const int64_t win0 = tok0 + rg.f + (T.w_lo - rg.w0);
+    auto half_row = [&](int h) -> int64_t {
+        if (h < h_e) return rg.base + h * HALF;
+        if (h < h_e + h_f) return tok0 + (h - h_e) * HALF;
+        // (an odd count: the last half repeats finite rows that no query sees)
+        return h < n_half ? win0 + (h - h_e - h_f) * HALF : win0;
+    };
+
+    if (tid == 0) {
+        for (int i = 0; i < NSLOT; ++i) { mbar_init(smem_u32(&c.full[i]), 1); mbar_init(smem_u32(&c.empty[i]), 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&c.s_full[i]), 1); mbar_init(smem_u32(&c.p_full[i]), 2 * NSOFT); }
+        mbar_init(smem_u32(&c.pv_done), 1);
+        mbar_init(smem_u32(&c.drain), 2);           // both issuing threads
+        c.abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&c.tmem)), "r"(TMEM_COLS) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+
+    // ---- this CTA's 64 query rows -> fp16, K-major; RMSNorm and RoPE in fp32.  The query is older than the
+    // staging kernel (a plain launch), so it may be read before the wait on it.
+    const int rbase = rank * ROWS;                  // first row of this CTA in the tile
+    const int rows = T.rows - rbase < 0 ? 0 : (T.rows - rbase < ROWS ? T.rows - rbase : ROWS);
+    const int tok_first = (T.r0 + rbase) / p.H;     // token (inside the request) of this CTA's row 0
+    const int tok_last = rows > 0 ? (T.r0 + rbase + rows - 1) / p.H : tok_first - 1;
+    float2* s_cs = reinterpret_cast<float2*>(smem + P_OFF);     // [token][32], while P is not in use
+    auto rope_table = [&]() {
+        for (int w = tid; w < (tok_last - tok_first + 1) * (DR / 2); w += NTHREADS)
+            s_cs[w] = rope_cs(p.inv_freq, w % (DR / 2), T.ctx + tok_first + w / (DR / 2));
+    };
+    if (p.inv_freq) { rope_table(); __syncthreads(); }
+    for (int r = warp; r < ROWS; r += NTHREADS / 32) {
+        uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (r < rows) {
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (T.row0 + rbase + r) * D + lane * 16);
+            *reinterpret_cast<uint4*>(v) = __ldg(src);
+            *reinterpret_cast<uint4*>(v + 4) = __ldg(src + 1);
+        }
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[i] << 16); f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u); }
+        if (p.q_norm_w) {
+            float ss = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ss += f[i] * f[i];
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) f[i] = f[i] * rr * __ldg(p.q_norm_w + lane * 16 + i);
+        }
+        if (p.inv_freq && r < rows && lane * 16 >= DN) {
+            const float2* cs = s_cs + ((T.r0 + rbase + r) / p.H - tok_first) * (DR / 2) + (lane * 16 - DN) / 2;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = f[2 * i], b = f[2 * i + 1];
+                f[2 * i] = a * cs[i].x - b * cs[i].y;
+                f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
+            }
+        }
+        uint8_t* blk = smem + Q_OFF + (lane >> 2) * 8192;
+        const int ch = (lane & 3) * 2;
+        *reinterpret_cast<uint4*>(blk + sw128(r, ch)) =
+            make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+        *reinterpret_cast<uint4*>(blk + sw128(r, ch + 1)) =
+            make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
+    }
+    fence_async();
+    fence_before();
+    __syncwarp();
+    cluster_sync();                                 // barriers, Q and TMEM of both CTAs are ready
+    fence_after();
+    pdl_wait();                                     // the staged rows are complete
+    const uint32_t tmem = c.tmem;
+    bool ok = true;
+
+    if (warp == 8) {
+        // ------------------------------------------------------------ TMA
+        const bool leader = elect_one();
+        auto piece = [&](int pos) -> uint32_t {      // waits for the ring slot, announces both CTAs' bytes
+            const int sl = pos % NSLOT;
+            if (pos >= NSLOT && ok) ok = wait_bar(smem_u32(&c.empty[sl]), ((pos / NSLOT) & 1) ^ 1, abort_flag);
+            if (ok && rank == 0 && leader) mbar_expect(smem_u32(&c.full[sl]), 2 * SLOT);
+            return sbase + R_OFF + sl * SLOT;
+        };
+        for (int i = 0; i <= n && ok; ++i) {
+            if (i < n) {
+                const int y = static_cast<int>(half_row(2 * i + rank));
+                for (int j = 0; j < 4 && ok; ++j) {
+                    const int pos = k_pos(i) + j;
+                    const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
+                    if (ok && leader) {
+                        tma_2d(dst, &k_map, j * 128, y, bar);
+                        tma_2d(dst + 8192, &k_map, j * 128 + 64, y, bar);
+                    }
+                }
+            }
+            if (i > 0) {
+                for (int j = 0; j < 4 && ok; ++j) {
+                    const int pos = v_pos(i - 1, n) + j;
+                    const int y = static_cast<int>(half_row(2 * (i - 1) + (j >> 1))) + (j & 1) * 32;
+                    const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
+                    if (ok && leader)
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) tma_2d(dst + b * 4096, &v_map, rank * 256 + b * 64, y, bar);
+                }
+            }
+        }
+        // gave up: copies in flight land within microseconds, before this CTA's memory may go to another
+        if (!ok) for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    } else if (warp == 9 && rank == 0) {
+        // ------------------------------------------------------------ QK issue
+        const bool leader = elect_one();
+        constexpr uint32_t id = idesc_f16(128, 128, 0);
+        const uint64_t qd = sdesc(sbase + Q_OFF, 16, 1024);
+        for (int i = 0; i < n && ok; ++i) {
+            // S buffer i & 1 was read by every softmax thread before it stored P(i - 2)
+            if (i >= 2) ok = wait_bar(smem_u32(&c.p_full[i & 1]), ((i - 2) >> 1) & 1, abort_flag);
+            for (int j = 0; j < 4 && ok; ++j) {
+                const int pos = k_pos(i) + j, sl = pos % NSLOT;
+                ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
+                if (!ok) break;
+                fence_after();
+                const uint64_t kd = sdesc(sbase + R_OFF + sl * SLOT, 16, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)   // 16 dims a step: column block kk / 4, 32 bytes a step inside it
+                        mma2(tmem + S_COL + (i & 1) * 64, qd + static_cast<uint32_t>(((2 * j + (kk >> 2)) * 8192 + (kk & 3) * 32) >> 4),
+                             kd + static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id, (j > 0 || kk > 0) ? 1u : 0u);
+                    commit2(smem_u32(&c.empty[sl]));
+                    if (j == 3) commit2(smem_u32(&c.s_full[i & 1]));
+                }
+                __syncwarp();
+            }
+        }
+        if (leader) commit2(smem_u32(&c.drain));
+    } else if (warp == 10 && rank == 0) {
+        // ------------------------------------------------------------ PV issue
+        const bool leader = elect_one();
+        constexpr uint32_t id = idesc_f16(128, 256, 1);
+        const uint64_t pd = sdesc(sbase + P_OFF, 16, 1024);
+        for (int i = 0; i < n && ok; ++i) {
+            ok = wait_bar(smem_u32(&c.p_full[i & 1]), (i >> 1) & 1, abort_flag);
+            for (int j = 0; j < 4 && ok; ++j) {
+                const int pos = v_pos(i, n) + j, sl = pos % NSLOT;
+                ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
+                if (!ok) break;
+                fence_after();
+                // V: dims are contiguous (MN-major), 64-dim column blocks 4096 B apart, 8 keys 1024 B
+                const uint64_t vd = sdesc(sbase + R_OFF + sl * SLOT, 4096, 1024);
+                if (leader) {
+#pragma unroll
+                    for (int k2 = 0; k2 < 2; ++k2) {
+                        const int kk = 2 * j + k2;   // 16 keys a step
+                        const uint64_t a = pd + static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            mma2(tmem + O_COL + h * 128, a, vd + static_cast<uint32_t>((h * 8192 + k2 * 2048) >> 4), id,
+                                 (i > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    commit2(smem_u32(&c.empty[sl]));
+                    if (j == 3) commit2(smem_u32(&c.pv_done));
+                }
+                __syncwarp();
+            }
+        }
+        if (leader) commit2(smem_u32(&c.drain));
+    } else if (warp < NSOFT) {
+        // ------------------------------------------------------------ softmax
+        const int qd = warp & 3, sub = warp >> 2;
+        const int hk = qd >> 1;                      // which half of the tile's keys
+        const int r = (qd & 1) * 32 + lane;          // row of this CTA
+        const int part = hk * 2 + sub;
+        const uint32_t lb = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+        const int rt = min(rbase + r, T.rows - 1);
+        const RowKeys rk = row_keys(p, T, T.ctx + (T.r0 + rt) / p.H);
+        const int w0s = T.n_e + T.n_f;               // first window slot
+        const uint32_t p_first[2] = {in_first(smem_u32(&c.p_full[0])), in_first(smem_u32(&c.p_full[1]))};
+        float m_used = -INFINITY, l_run = 0.0f;
+        auto flags_of = [&](int i) -> uint32_t {
+            return i < n ? s.flags[half_row(2 * i + hk) + sub * 32 + lane] : 0u;
+        };
+        uint32_t fl = flags_of(0);
+        for (int i = 0; i < n; ++i) {
+            const int h = 2 * i + hk;
+            // keys that this row sees among the thread's 32, as bits
+            const unsigned gone = __ballot_sync(0xffffffffu, fl & 1u), bad = __ballot_sync(0xffffffffu, fl & 2u);
+            auto below = [](int k) -> unsigned { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
+            unsigned vis;
+            if (h < h_e) {
+                vis = below(rk.e_lim - (h * HALF + sub * 32));
+            } else if (h < h_e + h_f) {
+                vis = below(T.n_f - ((h - h_e) * HALF + sub * 32));
+            } else {
+                const int k0 = w0s + (h - h_e - h_f) * HALF + sub * 32;       // slot of the thread's first key
+                vis = h < n_half ? below(rk.w_hi + 1 - k0) & (~below(rk.w_from - k0) | below(rk.f_to - k0)) : 0u;
+            }
+            vis &= ~gone;
+            fl = flags_of(i + 1);
+            if (ok) ok = wait_bar(smem_u32(&c.s_full[i & 1]), (i >> 1) & 1, abort_flag);
+            fence_after();
+            uint32_t sr[32];
+            tmem_ld32(lb + S_COL + (i & 1) * 64 + sub * 32, sr);
+            tmem_wait_ld();
+            float v[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sr[j]);
+            if (!__all_sync(0xffffffffu, vis == 0xffffffffu))
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = ((vis >> j) & 1u) ? v[j] : -INFINITY;
+            float t[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) t[j] = fmaxf(v[j], v[j + 16]);
+#pragma unroll
+            for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
+            c.mx[i & 1][part][r] = t[0];
+            bar_sync(1, NSOFT * 32);
+            // the scale is positive: the largest raw logit scaled is the largest logit
+            const float m_tile = fmaxf(fmaxf(c.mx[i & 1][0][r], c.mx[i & 1][1][r]),
+                                       fmaxf(c.mx[i & 1][2][r], c.mx[i & 1][3][r])) * p.scale_log2;
+            bool resc = false;
+            float alpha = 1.0f;
+            if (m_used == -INFINITY) {
+                m_used = m_tile;                     // nothing seen before: O and l are zero
+            } else if (m_tile > m_used + GROW) {
+                resc = true;
+                alpha = ex2(m_used - m_tile);
+                m_used = m_tile;
+            }
+            const float ref = m_used == -INFINITY ? 0.0f : m_used;
+            uint32_t pk[16];
+            float ps[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                pk[j] = pack_half2(ex2(fmaf(v[2 * j], p.scale_log2, -ref)), ex2(fmaf(v[2 * j + 1], p.scale_log2, -ref)));
+                const float2 f = unpack_half2(pk[j]);    // l sums the probabilities as PV uses them
+                ps[j] = f.x + f.y;
+            }
+#pragma unroll
+            for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                for (int j = 0; j < w; ++j) ps[j] += ps[j + w];
+            l_run = l_run * alpha + ps[0];
+            if (vis & bad) l_run = __int_as_float(0x7fc00000);   // a visible key that is not finite
+            if (i > 0 && ok) ok = wait_bar(smem_u32(&c.pv_done), (i - 1) & 1, abort_flag);   // P and O are free
+            if (__any_sync(0xffffffffu, resc) && ok) {
+                fence_after();
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t o[32];
+                    const uint32_t a = lb + O_COL + sub * 128 + q * 32;
+                    tmem_ld32(a, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                    tmem_st32(a, o);
+                }
+                tmem_wait_st();
+            }
+            uint8_t* pb = smem + P_OFF + hk * 8192;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(pb + sw128(r, sub * 4 + j)) =
+                    make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+            fence_async();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(p_first[i & 1]);
+        }
+        if (ok) ok = wait_bar(smem_u32(&c.pv_done), (n - 1) & 1, abort_flag);
+        fence_after();
+        c.l[part][r] = l_run;
+        // P's memory is free again: the RoPE table for the way back
+        if (p.inv_freq)
+            for (int w = tid; w < (tok_last - tok_first + 1) * (DR / 2); w += NSOFT * 32)
+                s_cs[w] = rope_cs(p.inv_freq, w % (DR / 2), T.ctx + tok_first + w / (DR / 2));
+        bar_sync(1, NSOFT * 32);
+        float l = c.l[0][r] + c.l[1][r] + c.l[2][r] + c.l[3][r];
+        if (p.sink && (m_used != -INFINITY || l != l)) l += ex2(__ldg(p.sink + (T.r0 + rt) % p.H) * LOG2E - m_used);
+        float inv = l == 0.0f ? 0.0f : 1.0f / l;
+        if (*abort_flag) inv = __int_as_float(0x7fc00000);
+        // O: row r, dims 256 hk + 128 sub .. + 127, as bf16 into the ring's memory (free: every piece was consumed),
+        // 16-byte chunks swizzled by row, then whole rows out
+        uint8_t* ob = smem + R_OFF;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+            uint32_t o[32];
+            tmem_ld32(lb + O_COL + sub * 128 + q * 32, o);
+            tmem_wait_ld();
+            float f[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
+            const int d0 = hk * 256 + sub * 128 + q * 32;
+            if (p.inv_freq && d0 >= DN) {
+                const float2* cs = s_cs + ((T.r0 + rt) / p.H - tok_first) * (DR / 2) + (d0 - DN) / 2;
+                if (r < rows)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float x = f[2 * j], y = f[2 * j + 1];
+                        f[2 * j] = x * cs[j].x + y * cs[j].y;
+                        f[2 * j + 1] = y * cs[j].x - x * cs[j].y;
+                    }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]);
+                    w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+                *reinterpret_cast<uint4*>(ob + r * 1024 + (((d0 / 8 + j) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        bar_sync(1, NSOFT * 32);
+        for (int rr = warp; rr < rows; rr += NSOFT) {
+            uint16_t* dst = p.out + (T.row0 + rbase + rr) * D;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int ch = k * 32 + lane;
+                *reinterpret_cast<uint4*>(dst + ch * 8) = *reinterpret_cast<const uint4*>(ob + rr * 1024 + ((ch ^ (rr & 7)) << 4));
+            }
+        }
+        fence_before();
+    }
+    __syncwarp();
+    // every issued MMA has completed before TMEM is freed and before either CTA's memory goes
+    if (warp == 9) {
+        const long long t0 = clock64();
+        while (!mbar_try(smem_u32(&c.drain), 0) && clock64() - t0 < WAIT_CLOCKS) {}
+        __syncwarp();
+    }
+    cluster_sync();
+    if (warp == 9) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM_COLS) : "memory");
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &q, cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(q);
+        return nullptr;
+    }();
+    return fn;
+}
+
+static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dim[2] = {D, static_cast<cuuint64_t>(bound)};
+    const cuuint64_t stride[1] = {D * 2};
+    const cuuint32_t box[2] = {64, box_rows}, ones[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace tcp
+
+// Workspace of the chunk kernels: staged rows (fp16), then a flag byte a row.
+static int64_t stage_per_req(int64_t max_entries, int W, int n_first) {
+    return ((max_entries + 63) & ~int64_t(63)) + n_first + W + 63;
+}
+int64_t tc_stage_rows(int64_t n_rows, int B, int64_t max_entries, int W, int n_first) {
+    return B * stage_per_req(max_entries, W, n_first) + n_rows;
+}
+size_t tc_stage_bytes(int64_t rows) { return (static_cast<size_t>(rows) * (tcp::D * 2 + 1) + 255) & ~size_t(255); }
+
+int tc_chunk_launch(const Params& p, int64_t max_entries, void* ws, cudaStream_t st) {
+    tcp::Stage s;
+    s.per_req = stage_per_req(max_entries, p.W, p.n_first);
+    s.bound = tc_stage_rows(p.n_rows, p.B, max_entries, p.W, p.n_first);
+    s.rows = static_cast<uint16_t*>(ws);
+    s.flags = reinterpret_cast<uint8_t*>(s.rows + s.bound * tcp::D);
+    CUtensorMap km, vm;
+    if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF) || !tcp::make_map(&vm, s.rows, s.bound, 32)) return HCA_ERR_CUDA;
+    cudaError_t e = cudaFuncSetAttribute(tcp::paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcp::SMEM);
+    if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
+    tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound, 8)), 256, 0, st>>>(p, s);
+    HCA_CHECK_LAUNCH();
+    const int64_t tiles = p.n_rows * p.H / tcp::PAIR + p.B;
+    e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * tiles)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm);
+    if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
+    HCA_CHECK_LAUNCH();
+    return HCA_OK;
+}
+
+}  // namespace paged
+
+// Reads and clears the device error word of the chunk kernel.  Synchronous.
+int paged_take_device_error() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_paged_device_error, sizeof(int)) != cudaSuccess) return -1;
+    if (v) {
+        const int z = 0;
+        cudaMemcpyToSymbol(g_paged_device_error, &z, sizeof(int));
+    }
+    return v;
+}
+
+}  // namespace hca
