@@ -87,7 +87,9 @@ struct Tile {
 
 __device__ __forceinline__ int64_t entries_before(const Params& p, int64_t pos) {
     if (p.m <= 0) return 0;
-    const int64_t e = (pos + 1) / p.m, cap = static_cast<int64_t>(p.e_width) * p.e_size;
+    // positions stay below 2^31
+    const int64_t e = static_cast<uint32_t>(pos + 1) / static_cast<uint32_t>(p.m);
+    const int64_t cap = static_cast<int64_t>(p.e_width) * p.e_size;
     return e < cap ? e : cap;
 }
 
@@ -106,7 +108,7 @@ __device__ __forceinline__ bool make_tile(const Params& p, int64_t t, int R, Til
     T.rows = static_cast<int>(left < R ? left : R);
     T.row0 = s * p.H + r0;
     T.ctx = p.ctx[b] > 0 ? p.ctx[b] : 0;
-    const int64_t p_lo = T.ctx + r0 / p.H, p_hi = T.ctx + (r0 + T.rows - 1) / p.H;
+    const int64_t p_lo = T.ctx + T.r0 / p.H, p_hi = T.ctx + (T.r0 + T.rows - 1) / p.H;
     T.w_lo = p_lo - (p.W - 1) > 0 ? p_lo - (p.W - 1) : 0;
     T.n_e = static_cast<int>(entries_before(p, p_hi));
     T.n_f = static_cast<int>(p.n_first < T.w_lo ? p.n_first : T.w_lo);
@@ -156,11 +158,18 @@ __device__ __forceinline__ bool bad_half2(uint32_t h) {
     return (h & 0x7C00u) == 0x7C00u || (h & 0x7C000000u) == 0x7C000000u;
 }
 
-// cos / sin of RoPE pair i at position t (fp64 angle t f_i, exact; fp32 out)
+// cos / sin of RoPE pair i at position t, fp32 out.  The angle t f_i is exact in
+// fp64 (31 + 24 bits); its whole half turns are taken off there (the product
+// with 1 / pi is off by 2^-53 of itself: below 2^-24 of a half turn for every
+// position), and the rest, in [-1/2, 1/2] half turns, goes to sincospif.  An
+// fp64 sincos costs 16K clocks of latency here, more than the query's load.
 __device__ __forceinline__ float2 rope_cs(const float* inv_freq, int i, int64_t t) {
-    double sn, cs;
-    sincos(static_cast<double>(t) * static_cast<double>(__ldg(inv_freq + i)), &sn, &cs);
-    return make_float2(static_cast<float>(cs), static_cast<float>(sn));
+    const double u = static_cast<double>(t) * static_cast<double>(__ldg(inv_freq + i)) * 0.31830988618379067154;
+    const double k = rint(u);
+    float sn, cs;
+    sincospif(static_cast<float>(u - k), &sn, &cs);
+    if (static_cast<long long>(k) & 1) { sn = -sn; cs = -cs; }
+    return make_float2(cs, sn);
 }
 
 __device__ __forceinline__ float ex2(float x) {

@@ -27,8 +27,8 @@
 // 16 KB pieces of one ring of 8, consumed in the order QK(0), QK(i + 1), PV(i),
 // ...: the softmax of tile i runs beside QK(i + 1).
 //
-// Warps: 0-7 softmax and output (a row is shared by 4 threads: 2 TMEM lanes x 2
-// column halves), 8 TMA, 9 QK issue, 10 PV issue (the first CTA's only).
+// Warps: 0-7 query, softmax and output (two groups of four, tiles in turn; a
+// row of a tile is shared by two threads, one TMEM lane each), 8 TMA, 9 QK issue, 10 PV issue (the first CTA's only).
 // The online softmax is in base 2; O is rescaled only when a row's maximum
 // grows by more than 2^8 (P <= 2^8 in fp16).  Every wait is bounded: one that
 // gives up sets the device error word, the CTA's outputs become NaN, and the
@@ -50,9 +50,10 @@ constexpr int ROWS = 64;                     // rows of one CTA
 constexpr int HALF = 64;                     // keys of a half tile (one CTA's K)
 constexpr int NSLOT = 8, SLOT = 16384;
 constexpr int Q_OFF = 0;                     // 8 column blocks (64 dims) of 64 rows x 128 B
-constexpr int P_OFF = 65536;                 // 2 column blocks (64 keys) of 64 rows x 128 B
-constexpr int R_OFF = P_OFF + 16384;
-constexpr int SMEM = R_OFF + NSLOT * SLOT + 1024;
+constexpr int P_OFF = 65536;                 // 2 buffers of 2 column blocks (64 keys) of 64 rows x 128 B
+constexpr int R_OFF = P_OFF + 2 * 16384;
+constexpr int CTRL_OFF = R_OFF + NSLOT * SLOT;
+constexpr int SMEM = 232448;                 // all that a CTA may have: the rest is Ctrl's
 constexpr int NSOFT = 8, NTHREADS = 11 * 32;
 constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 512;
 constexpr float GROW = 8.0f;                 // log2 units
@@ -215,7 +216,7 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void bar_sync(int id, int n) { asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(n) : "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -273,18 +274,19 @@ __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 8 * i - 4; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 8 * i + 4 : 8 * i + 8; }
 
 struct Ctrl {
-    uint64_t full[NSLOT], empty[NSLOT], s_full[2], p_full[2], pv_done, drain;
-    float mx[2][4][ROWS];
+    uint64_t full[NSLOT], empty[NSLOT], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
+    float mx[2][2][ROWS];       // [group][key half][row]: a tile's largest raw logit
+    float m[2][ROWS];           // [tile parity][row]: the running maximum (base 2) after the tile
     float l[4][ROWS];
     uint32_t tmem;
     int abort_flag;
 };
+static_assert(CTRL_OFF + sizeof(Ctrl) <= SMEM, "shared memory");
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(16) Ctrl c;
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];
+    Ctrl& c = *reinterpret_cast<Ctrl*>(smem + CTRL_OFF);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t rank = cta_rank();
     const uint32_t sbase = smem_u32(smem);
@@ -308,8 +310,13 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
 
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) { mbar_init(smem_u32(&c.full[i]), 1); mbar_init(smem_u32(&c.empty[i]), 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(smem_u32(&c.s_full[i]), 1); mbar_init(smem_u32(&c.p_full[i]), 2 * NSOFT); }
-        mbar_init(smem_u32(&c.pv_done), 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c.s_full[i]), 1);
+            mbar_init(smem_u32(&c.s_free[i]), NSOFT);   // the four warps of the tile's group, in both CTAs
+            mbar_init(smem_u32(&c.p_full[i]), NSOFT);
+            mbar_init(smem_u32(&c.pv_done[i]), 1);
+        }
+        mbar_init(smem_u32(&c.q_full), 2 * NSOFT);
         mbar_init(smem_u32(&c.drain), 2);           // both issuing threads
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -319,65 +326,18 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
 
-    // ---- this CTA's 64 query rows -> fp16, K-major; RMSNorm and RoPE in fp32.  The query is older than the
-    // staging kernel (a plain launch), so it may be read before the wait on it.
-    const int rbase = rank * ROWS;                  // first row of this CTA in the tile
-    const int rows = T.rows - rbase < 0 ? 0 : (T.rows - rbase < ROWS ? T.rows - rbase : ROWS);
-    const int tok_first = (T.r0 + rbase) / p.H;     // token (inside the request) of this CTA's row 0
-    const int tok_last = rows > 0 ? (T.r0 + rbase + rows - 1) / p.H : tok_first - 1;
-    float2* s_cs = reinterpret_cast<float2*>(smem + P_OFF);     // [token][32], while P is not in use
-    auto rope_table = [&]() {
-        for (int w = tid; w < (tok_last - tok_first + 1) * (DR / 2); w += NTHREADS)
-            s_cs[w] = rope_cs(p.inv_freq, w % (DR / 2), T.ctx + tok_first + w / (DR / 2));
-    };
-    if (p.inv_freq) { rope_table(); __syncthreads(); }
-    for (int r = warp; r < ROWS; r += NTHREADS / 32) {
-        uint32_t v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (r < rows) {
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (T.row0 + rbase + r) * D + lane * 16);
-            *reinterpret_cast<uint4*>(v) = __ldg(src);
-            *reinterpret_cast<uint4*>(v + 4) = __ldg(src + 1);
-        }
-        float f[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[i] << 16); f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u); }
-        if (p.q_norm_w) {
-            float ss = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) ss += f[i] * f[i];
-#pragma unroll
-            for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = f[i] * rr * __ldg(p.q_norm_w + lane * 16 + i);
-        }
-        if (p.inv_freq && r < rows && lane * 16 >= DN) {
-            const float2* cs = s_cs + ((T.r0 + rbase + r) / p.H - tok_first) * (DR / 2) + (lane * 16 - DN) / 2;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = f[2 * i], b = f[2 * i + 1];
-                f[2 * i] = a * cs[i].x - b * cs[i].y;
-                f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
-            }
-        }
-        uint8_t* blk = smem + Q_OFF + (lane >> 2) * 8192;
-        const int ch = (lane & 3) * 2;
-        *reinterpret_cast<uint4*>(blk + sw128(r, ch)) =
-            make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-        *reinterpret_cast<uint4*>(blk + sw128(r, ch + 1)) =
-            make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
-    }
-    fence_async();
     fence_before();
-    __syncwarp();
-    cluster_sync();                                 // barriers, Q and TMEM of both CTAs are ready
+    __syncthreads();
+    cluster_sync();                                 // barriers and TMEM of both CTAs are ready
     fence_after();
-    pdl_wait();                                     // the staged rows are complete
     const uint32_t tmem = c.tmem;
     bool ok = true;
+    const int rbase = rank * ROWS;                  // first row of this CTA in the tile
+    const int rows = T.rows - rbase < 0 ? 0 : (T.rows - rbase < ROWS ? T.rows - rbase : ROWS);
 
     if (warp == 8) {
         // ------------------------------------------------------------ TMA
+        pdl_wait();                                 // the staged rows are complete
         const bool leader = elect_one();
         auto piece = [&](int pos) -> uint32_t {      // waits for the ring slot, announces both CTAs' bytes
             const int sl = pos % NSLOT;
@@ -415,9 +375,10 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_f16(128, 128, 0);
         const uint64_t qd = sdesc(sbase + Q_OFF, 16, 1024);
+        ok = wait_bar(smem_u32(&c.q_full), 0, abort_flag);
         for (int i = 0; i < n && ok; ++i) {
-            // S buffer i & 1 was read by every softmax thread before it stored P(i - 2)
-            if (i >= 2) ok = wait_bar(smem_u32(&c.p_full[i & 1]), ((i - 2) >> 1) & 1, abort_flag);
+            // S(i - 2) has been read
+            if (i >= 2) ok = wait_bar(smem_u32(&c.s_free[i & 1]), ((i - 2) >> 1) & 1, abort_flag);
             for (int j = 0; j < 4 && ok; ++j) {
                 const int pos = k_pos(i) + j, sl = pos % NSLOT;
                 ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
@@ -454,105 +415,195 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
 #pragma unroll
                     for (int k2 = 0; k2 < 2; ++k2) {
                         const int kk = 2 * j + k2;   // 16 keys a step
-                        const uint64_t a = pd + static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
+                        const uint64_t a = pd + static_cast<uint32_t>(((i & 1) * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             mma2(tmem + O_COL + h * 128, a, vd + static_cast<uint32_t>((h * 8192 + k2 * 2048) >> 4), id,
                                  (i > 0 || kk > 0) ? 1u : 0u);
                     }
                     commit2(smem_u32(&c.empty[sl]));
-                    if (j == 3) commit2(smem_u32(&c.pv_done));
+                    if (j == 3) commit2(smem_u32(&c.pv_done[i & 1]));
                 }
                 __syncwarp();
             }
         }
         if (leader) commit2(smem_u32(&c.drain));
     } else if (warp < NSOFT) {
+        // ---- this CTA's 64 query rows -> fp16, K-major, 8 rows a warp, every load in flight before the first use;
+        // RMSNorm and RoPE in fp32.  The query is older than the staging kernel (a plain launch): it may be read
+        // before the wait on that kernel.
+        {
+            uint32_t v[8][8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = warp * 8 + k;
+                if (r < rows) {
+                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (T.row0 + rbase + r) * D + lane * 16);
+                    *reinterpret_cast<uint4*>(v[k]) = __ldg(src);
+                    *reinterpret_cast<uint4*>(v[k] + 4) = __ldg(src + 1);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[k][i] = 0;
+                }
+            }
+            int tok = -1;
+            float2 cs = make_float2(1.0f, 0.0f);        // of pair `lane` at the row's position
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int r = warp * 8 + k;
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[k][i] << 16); f[2 * i + 1] = __uint_as_float(v[k][i] & 0xFFFF0000u); }
+                if (p.q_norm_w) {
+                    float ss = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) ss += f[i] * f[i];
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 nw = __ldg(reinterpret_cast<const float4*>(p.q_norm_w + lane * 16 + i));
+                        f[i] *= rr * nw.x; f[i + 1] *= rr * nw.y; f[i + 2] *= rr * nw.z; f[i + 3] *= rr * nw.w;
+                    }
+                }
+                if (p.inv_freq && r < rows) {
+                    const int tk = (T.r0 + rbase + r) / p.H;
+                    if (tk != tok) { tok = tk; cs = rope_cs(p.inv_freq, lane, T.ctx + tk); }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int pair = ((lane * 16 - DN) / 2 + i) & 31;
+                        const float x = __shfl_sync(0xffffffffu, cs.x, pair), y = __shfl_sync(0xffffffffu, cs.y, pair);
+                        if (lane * 16 >= DN) {
+                            const float a = f[2 * i], b = f[2 * i + 1];
+                            f[2 * i] = a * x - b * y;
+                            f[2 * i + 1] = a * y + b * x;
+                        }
+                    }
+                }
+                uint8_t* blk = smem + Q_OFF + (lane >> 2) * 8192;
+                const int ch = (lane & 3) * 2;
+                *reinterpret_cast<uint4*>(blk + sw128(r, ch)) =
+                    make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                *reinterpret_cast<uint4*>(blk + sw128(r, ch + 1)) =
+                    make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.q_full)));
+        }
+        pdl_wait();                                  // (the flags of the staged rows)
+
         // ------------------------------------------------------------ softmax
-        const int qd = warp & 3, sub = warp >> 2;
+        // Group g (4 warps) takes the tiles of parity g, so that a tile's
+        // exponentials and its P stores run beside the next tile's; only the
+        // running maximum passes from tile to tile.
+        const int qd = warp & 3, g = warp >> 2;
         const int hk = qd >> 1;                      // which half of the tile's keys
         const int r = (qd & 1) * 32 + lane;          // row of this CTA
-        const int part = hk * 2 + sub;
         const uint32_t lb = tmem + (static_cast<uint32_t>(qd * 32) << 16);
         const int rt = min(rbase + r, T.rows - 1);
         const RowKeys rk = row_keys(p, T, T.ctx + (T.r0 + rt) / p.H);
         const int w0s = T.n_e + T.n_f;               // first window slot
-        const uint32_t p_first[2] = {in_first(smem_u32(&c.p_full[0])), in_first(smem_u32(&c.p_full[1]))};
-        float m_used = -INFINITY, l_run = 0.0f;
-        auto flags_of = [&](int i) -> uint32_t {
-            return i < n ? s.flags[half_row(2 * i + hk) + sub * 32 + lane] : 0u;
+        const uint32_t p_first = in_first(smem_u32(&c.p_full[g])), s_first = in_first(smem_u32(&c.s_free[g]));
+        float m_l = -INFINITY, l_run = 0.0f;         // this thread's share of l, and the maximum it is relative to
+        uint32_t fl[2];
+        auto flags_of = [&](int i) {
+            const uint8_t* f = s.flags + (i < n ? half_row(2 * i + hk) : rg.base) + lane;
+            fl[0] = f[0];
+            fl[1] = f[32];
         };
-        uint32_t fl = flags_of(0);
-        for (int i = 0; i < n; ++i) {
+        flags_of(g);
+        for (int i = g; i < n; i += 2) {
             const int h = 2 * i + hk;
-            // keys that this row sees among the thread's 32, as bits
-            const unsigned gone = __ballot_sync(0xffffffffu, fl & 1u), bad = __ballot_sync(0xffffffffu, fl & 2u);
+            // keys that this row sees among the half tile's 64, as bits
             auto below = [](int k) -> unsigned { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
-            unsigned vis;
-            if (h < h_e) {
-                vis = below(rk.e_lim - (h * HALF + sub * 32));
-            } else if (h < h_e + h_f) {
-                vis = below(T.n_f - ((h - h_e) * HALF + sub * 32));
-            } else {
-                const int k0 = w0s + (h - h_e - h_f) * HALF + sub * 32;       // slot of the thread's first key
-                vis = h < n_half ? below(rk.w_hi + 1 - k0) & (~below(rk.w_from - k0) | below(rk.f_to - k0)) : 0u;
+            unsigned vis[2], bad = 0;
+#pragma unroll
+            for (int z = 0; z < 2; ++z) {
+                const unsigned gone = __ballot_sync(0xffffffffu, fl[z] & 1u), nf = __ballot_sync(0xffffffffu, fl[z] & 2u);
+                if (h < h_e) {
+                    vis[z] = below(rk.e_lim - (h * HALF + z * 32));
+                } else if (h < h_e + h_f) {
+                    vis[z] = below(T.n_f - ((h - h_e) * HALF + z * 32));
+                } else {
+                    const int k0 = w0s + (h - h_e - h_f) * HALF + z * 32;     // slot of the first of these keys
+                    vis[z] = h < n_half ? below(rk.w_hi + 1 - k0) & (~below(rk.w_from - k0) | below(rk.f_to - k0)) : 0u;
+                }
+                vis[z] &= ~gone;
+                bad |= vis[z] & nf;
             }
-            vis &= ~gone;
-            fl = flags_of(i + 1);
-            if (ok) ok = wait_bar(smem_u32(&c.s_full[i & 1]), (i >> 1) & 1, abort_flag);
+            flags_of(i + 2);
+            if (ok) ok = wait_bar(smem_u32(&c.s_full[g]), (i >> 1) & 1, abort_flag);
             fence_after();
-            uint32_t sr[32];
-            tmem_ld32(lb + S_COL + (i & 1) * 64 + sub * 32, sr);
-            tmem_wait_ld();
-            float v[32];
+            float v[64];
+            {
+                uint32_t sr[32];
+                tmem_ld32(lb + S_COL + g * 64, sr);
+                uint32_t s2[32];
+                tmem_ld32(lb + S_COL + g * 64 + 32, s2);
+                tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(sr[j]);
-            if (!__all_sync(0xffffffffu, vis == 0xffffffffu))
+                for (int j = 0; j < 32; ++j) { v[j] = __uint_as_float(sr[j]); v[32 + j] = __uint_as_float(s2[j]); }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(s_first);            // S may be overwritten
+            if (!__all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu))
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = ((vis >> j) & 1u) ? v[j] : -INFINITY;
+                for (int j = 0; j < 64; ++j) v[j] = ((vis[j >> 5] >> (j & 31)) & 1u) ? v[j] : -INFINITY;
             float t[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) t[j] = fmaxf(v[j], v[j + 16]);
+            for (int j = 0; j < 16; ++j) t[j] = fmaxf(fmaxf(v[j], v[j + 16]), fmaxf(v[j + 32], v[j + 48]));
 #pragma unroll
             for (int w = 8; w >= 1; w >>= 1)
 #pragma unroll
                 for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
-            c.mx[i & 1][part][r] = t[0];
-            bar_sync(1, NSOFT * 32);
+            c.mx[g][hk][r] = t[0];
+            bar_sync(1 + g, 128);
             // the scale is positive: the largest raw logit scaled is the largest logit
-            const float m_tile = fmaxf(fmaxf(c.mx[i & 1][0][r], c.mx[i & 1][1][r]),
-                                       fmaxf(c.mx[i & 1][2][r], c.mx[i & 1][3][r])) * p.scale_log2;
+            const float m_tile = fmaxf(t[0], c.mx[g][hk ^ 1][r]) * p.scale_log2;
+            // the maximum after tile i - 1, from the other group
+            // (a barrier of this group either way, before c.mx is written again)
+            if (i > 0) bar_sync(3 + (i & 1), 256); else bar_sync(1 + g, 128);
+            const float m_old = i > 0 ? c.m[(i - 1) & 1][r] : -INFINITY;
             bool resc = false;
-            float alpha = 1.0f;
-            if (m_used == -INFINITY) {
-                m_used = m_tile;                     // nothing seen before: O and l are zero
-            } else if (m_tile > m_used + GROW) {
+            float m_new = m_old;
+            if (m_old == -INFINITY) {
+                m_new = m_tile;                      // nothing seen before: O and l are zero
+            } else if (m_tile > m_old + GROW) {
                 resc = true;
-                alpha = ex2(m_used - m_tile);
-                m_used = m_tile;
+                m_new = m_tile;
             }
-            const float ref = m_used == -INFINITY ? 0.0f : m_used;
-            uint32_t pk[16];
+            if (hk == 0) c.m[i & 1][r] = m_new;
+            if (i + 1 < n) asm volatile("bar.arrive %0, 256;" :: "r"(3 + ((i + 1) & 1)) : "memory");
+            const float ref = m_new == -INFINITY ? 0.0f : m_new;
+            uint32_t pk[32];
             float ps[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
+            for (int j = 0; j < 32; ++j) {
                 pk[j] = pack_half2(ex2(fmaf(v[2 * j], p.scale_log2, -ref)), ex2(fmaf(v[2 * j + 1], p.scale_log2, -ref)));
                 const float2 f = unpack_half2(pk[j]);    // l sums the probabilities as PV uses them
-                ps[j] = f.x + f.y;
+                if (j < 16) ps[j] = f.x + f.y; else ps[j - 16] += f.x + f.y;
             }
 #pragma unroll
             for (int w = 8; w >= 1; w >>= 1)
 #pragma unroll
                 for (int j = 0; j < w; ++j) ps[j] += ps[j + w];
-            l_run = l_run * alpha + ps[0];
-            if (vis & bad) l_run = __int_as_float(0x7fc00000);   // a visible key that is not finite
-            if (i > 0 && ok) ok = wait_bar(smem_u32(&c.pv_done), (i - 1) & 1, abort_flag);   // P and O are free
-            if (__any_sync(0xffffffffu, resc) && ok) {
+            l_run = (m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_new)) + ps[0];
+            m_l = m_new;
+            if (bad) l_run = __int_as_float(0x7fc00000);             // a visible key that is not finite
+            if (i >= 2 && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), ((i - 2) >> 1) & 1, abort_flag);   // P's buffer is free
+            if (__any_sync(0xffffffffu, resc)) {
+                // O must hold still: PV(i - 1) complete (PV(i - 3), the barrier's phase before, completed ahead of
+                // PV(i - 2), which has been waited for; PV(i) waits for this P)
+                if (ok) ok = wait_bar(smem_u32(&c.pv_done[g ^ 1]), ((i - 1) >> 1) & 1, abort_flag);
                 fence_after();
+                const float alpha = resc ? ex2(m_old - m_new) : 1.0f;
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 8; ++q) {
                     uint32_t o[32];
-                    const uint32_t a = lb + O_COL + sub * 128 + q * 32;
+                    const uint32_t a = lb + O_COL + q * 32;
                     tmem_ld32(a, o);
                     tmem_wait_ld();
 #pragma unroll
@@ -561,24 +612,30 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 }
                 tmem_wait_st();
             }
-            uint8_t* pb = smem + P_OFF + hk * 8192;
+            uint8_t* pb = smem + P_OFF + g * 16384 + hk * 8192;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(pb + sw128(r, sub * 4 + j)) =
-                    make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+            for (int j = 0; j < 8; ++j)
+                *reinterpret_cast<uint4*>(pb + sw128(r, j)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
             fence_async();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(p_first[i & 1]);
+            if (lane == 0) mbar_arrive_cluster(p_first);
         }
-        if (ok) ok = wait_bar(smem_u32(&c.pv_done), (n - 1) & 1, abort_flag);
+        // the last tile's group waits for the last PV (it has seen the phase before; the other group may not have)
+        if (g == ((n - 1) & 1) && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), ((n - 1) >> 1) & 1, abort_flag);
+        bar_sync(5, NSOFT * 32);
         fence_after();
-        c.l[part][r] = l_run;
+        const float m_used = c.m[(n - 1) & 1][r];
+        c.l[hk * 2 + g][r] = m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_used);
+        const int sub = g;                           // the half of the row's dims that this thread writes out
         // P's memory is free again: the RoPE table for the way back
+        const int tok_first = (T.r0 + rbase) / p.H;  // token (inside the request) of this CTA's row 0
+        const int tok_last = rows > 0 ? (T.r0 + rbase + rows - 1) / p.H : tok_first - 1;
+        float2* s_cs = reinterpret_cast<float2*>(smem + P_OFF);     // [token][32]
         if (p.inv_freq)
             for (int w = tid; w < (tok_last - tok_first + 1) * (DR / 2); w += NSOFT * 32)
                 s_cs[w] = rope_cs(p.inv_freq, w % (DR / 2), T.ctx + tok_first + w / (DR / 2));
-        bar_sync(1, NSOFT * 32);
+        bar_sync(5, NSOFT * 32);
         float l = c.l[0][r] + c.l[1][r] + c.l[2][r] + c.l[3][r];
         if (p.sink && (m_used != -INFINITY || l != l)) l += ex2(__ldg(p.sink + (T.r0 + rt) % p.H) * LOG2E - m_used);
         float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -616,7 +673,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 *reinterpret_cast<uint4*>(ob + r * 1024 + (((d0 / 8 + j) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
         }
-        bar_sync(1, NSOFT * 32);
+        bar_sync(5, NSOFT * 32);
         for (int rr = warp; rr < rows; rr += NSOFT) {
             uint16_t* dst = p.out + (T.row0 + rbase + rr) * D;
 #pragma unroll
