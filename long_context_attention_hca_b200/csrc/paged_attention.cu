@@ -45,8 +45,19 @@ struct Rows {
     static constexpr size_t K_BYTES = size_t(TK) * D * 2;
     static constexpr size_t P_BYTES = size_t(R) * TK * 2;
     static constexpr size_t CS_BYTES = size_t(R) * (DR / 2) * 8;     // cos / sin of each row's position
-    static constexpr size_t SMEM = Q_BYTES + K_BYTES + P_BYTES + CS_BYTES;
+    static constexpr size_t RAW_BYTES = size_t(TK) * D * 2;          // the next tile's keys as stored
+    static constexpr size_t SC_BYTES = size_t(TK) * 8 * 4;           // and their scales
+    static constexpr size_t SMEM = Q_BYTES + K_BYTES + P_BYTES + CS_BYTES + RAW_BYTES + SC_BYTES;
 };
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // row-major fp16 tile, 16-byte chunks XOR-swizzled by row (conflict-free ldmatrix)
 template <int W2>
@@ -78,6 +89,8 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     char* ks = smem + C::Q_BYTES;
     char* ps = ks + C::K_BYTES;
     float2* s_cs = reinterpret_cast<float2*>(ps + C::P_BYTES);
+    char* raw = ps + C::P_BYTES + C::CS_BYTES;
+    float* s_sc = reinterpret_cast<float*>(raw + C::RAW_BYTES);      // [key][8]
     __shared__ float s_max[8][16];               // [warp][row of its group]
     __shared__ float s_l[8][16];
     __shared__ float s_add[TK];                  // -inf: no such key; NaN: the key holds a non-finite value
@@ -94,6 +107,66 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     const int t_begin = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.n_splits);
     const int t_end = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.n_splits);
 
+    // ---- keys: a thread copies 16-dim unit u of keys kr + KPP k as stored (cp.async), and later converts just what it
+    // copied itself (no barrier in between).  The copies of a tile fly while the tile before is computed, its page
+    // numbers one tile ahead of that.
+    constexpr int UPK = D / 16;                  // 16-dim units of a key
+    constexpr int KPP = 256 / UPK;               // keys per pass
+    constexpr int NP = TK / KPP;                 // passes of a tile
+    const int u = tid % UPK, kr = tid / UPK, d0 = u * 16;
+    const uint32_t raw_a = static_cast<uint32_t>(__cvta_generic_to_shared(raw));
+    const uint32_t sc_a = static_cast<uint32_t>(__cvta_generic_to_shared(s_sc));
+    int32_t page[NP];                            // page number of the keys of the tile to copy next
+    auto slot_token = [&](int slot) -> uint32_t {
+        const int j = slot - T.n_e;
+        return static_cast<uint32_t>(j < T.n_f ? j : T.w_lo + (j - T.n_f));
+    };
+    auto fetch_pages = [&](int t) {
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int slot = t * TK + k * KPP + kr;
+            page[k] = -1;
+            if (t < t_end && slot < T.n_tot) {
+                const bool ent = slot < T.n_e;
+                const uint32_t i = ent ? static_cast<uint32_t>(slot) : slot_token(slot);
+                const uint32_t c = i / (ent ? p.e_size : p.t_size), w = ent ? p.e_width : p.t_width;
+                if (c < w) page[k] = __ldg((ent ? p.e_table : p.t_table) + static_cast<size_t>(T.b) * w + c);
+            }
+        }
+    };
+    // bit k: key k of the thread exists (a page inside the pool)
+    auto copy_tile = [&](int t) -> unsigned {
+        unsigned have = 0;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            const int key = k * KPP + kr, slot = t * TK + key;
+            const bool ent = slot < T.n_e;
+            if (page[k] < 0 || page[k] >= (ent ? p.e_pages : p.t_pages)) continue;
+            have |= 1u << k;
+            if (ent) {
+                const int64_t row = static_cast<int64_t>(page[k]) * p.e_size + static_cast<uint32_t>(slot) % p.e_size;
+                if (d0 < C::DN) {
+                    cp16(raw_a + key * (D * 2) + u * 32, p.codes + row * C::DN + d0);
+                    if (u % (C::G / 16) == 0) cp4(sc_a + (key * 8 + u / (C::G / 16)) * 4, p.scales + row * (C::DN / C::G) + u / (C::G / 16));
+                } else {
+                    const uint16_t* src = p.rope + row * C::DR + (d0 - C::DN);
+                    cp16(raw_a + key * (D * 2) + u * 32, src);
+                    cp16(raw_a + key * (D * 2) + u * 32 + 16, src + 8);
+                }
+            } else {
+                const int64_t row = static_cast<int64_t>(page[k]) * p.t_size + slot_token(slot) % p.t_size;
+                const uint16_t* src = p.tok + row * D + d0;
+                cp16(raw_a + key * (D * 2) + u * 32, src);
+                cp16(raw_a + key * (D * 2) + u * 32 + 16, src + 8);
+            }
+        }
+        cp_commit();
+        return have;
+    };
+    fetch_pages(t_begin);
+    unsigned have = copy_tile(t_begin);
+    fetch_pages(t_begin + 1);
+
     // ---- queries -> fp16 (rows past the last are zero); RMSNorm and RoPE in fp32
     if (p.inv_freq) {
         for (int w = tid; w < T.rows * (C::DR / 2); w += 256) {
@@ -104,21 +177,28 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
         }
         __syncthreads();
     }
-    for (int r = warp; r < R; r += 8) {
-        constexpr int CL = D / 32;               // consecutive dims of a lane
-        uint32_t v[CL / 2];
+    constexpr int CL = D / 32;                   // consecutive dims of a lane
+    uint32_t qv[R / 8][CL / 2];                  // every load in flight before the first use
 #pragma unroll
-        for (int i = 0; i < CL / 2; ++i) v[i] = 0;
+    for (int k = 0; k < R / 8; ++k) {
+        const int r = warp + 8 * k;
+#pragma unroll
+        for (int i = 0; i < CL / 2; ++i) qv[k][i] = 0;
         if (r < T.rows) {
             const uint16_t* src = p.q + (T.row0 + r) * D + lane * CL;
             if constexpr (CL >= 8) {
 #pragma unroll
                 for (int i = 0; i < CL / 8; ++i)
-                    *reinterpret_cast<uint4*>(v + 4 * i) = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    *reinterpret_cast<uint4*>(qv[k] + 4 * i) = __ldg(reinterpret_cast<const uint4*>(src) + i);
             } else {
-                *reinterpret_cast<uint2*>(v) = __ldg(reinterpret_cast<const uint2*>(src));
+                *reinterpret_cast<uint2*>(qv[k]) = __ldg(reinterpret_cast<const uint2*>(src));
             }
         }
+    }
+#pragma unroll
+    for (int k = 0; k < R / 8; ++k) {
+        const int r = warp + 8 * k;
+        uint32_t (&v)[CL / 2] = qv[k];
         float f[CL];
 #pragma unroll
         for (int i = 0; i < CL / 2; ++i) {
@@ -170,64 +250,52 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     for (int j = 0; j < C::NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.0f, 0.0f};
 
-    constexpr int UPK = D / 16;                  // 16-dim units of a key
-    constexpr int KPP = 256 / UPK;               // keys per pass
-    const int u = tid % UPK, kr = tid / UPK, d0 = u * 16;
     for (int t = t_begin; t < t_end; ++t) {
+        cp_wait();
         __syncthreads();                         // the last tile's keys and P are read
         bool flagged = false;
 #pragma unroll
-        for (int k0 = 0; k0 < TK; k0 += KPP) {
-            const int key = k0 + kr, slot = t * TK + key;
-            uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            int64_t row = -1;
-            if (slot < T.n_e) {
-                row = entry_row(p, T.b, slot);
-                if (row >= 0) {
-                    if (d0 < C::DN) {
-                        const uint4 cv = __ldg(reinterpret_cast<const uint4*>(p.codes + row * C::DN + d0));
-                        const float sc = __ldg(p.scales + row * (C::DN / C::G) + d0 / C::G);
-                        const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+        for (int k = 0; k < NP; ++k) {
+            const int key = k * KPP + kr, slot = t * TK + key;
+            const bool here = (have >> k) & 1u;
+            uint32_t h[8];
+            const uint4 r0 = *reinterpret_cast<const uint4*>(raw + key * (D * 2) + u * 32);
+            if (slot < T.n_e && d0 < C::DN) {
+                const float sc = s_sc[key * 8 + u / (C::G / 16)];
+                const uint32_t cw[4] = {r0.x, r0.y, r0.z, r0.w};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] & 0xFFFFu)));
-                            const float2 b = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] >> 16)));
-                            h[2 * i] = pack_half2(a.x * sc, a.y * sc);
-                            h[2 * i + 1] = pack_half2(b.x * sc, b.y * sc);
-                        }
-                    } else {
-                        const uint4* rp = reinterpret_cast<const uint4*>(p.rope + row * C::DR + (d0 - C::DN));
-                        const uint4 v0 = __ldg(rp), v1 = __ldg(rp + 1);
-                        const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] & 0xFFFFu)));
+                    const float2 b = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] >> 16)));
+                    h[2 * i] = pack_half2(a.x * sc, a.y * sc);
+                    h[2 * i + 1] = pack_half2(b.x * sc, b.y * sc);
                 }
-            } else if (slot < T.n_tot) {
-                const int j = slot - T.n_e;
-                row = token_row(p, T.b, static_cast<uint32_t>(j < T.n_f ? j : T.w_lo + (j - T.n_f)));
-                if (row >= 0) {
-                    const uint4* rp = reinterpret_cast<const uint4*>(p.tok + row * D + d0);
-                    const uint4 v0 = __ldg(rp), v1 = __ldg(rp + 1);
-                    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+            } else {
+                const uint4 r1 = *reinterpret_cast<const uint4*>(raw + key * (D * 2) + u * 32 + 16);
+                const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
-                }
+                for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
             }
             bool bad = false;
 #pragma unroll
             for (int i = 0; i < 8; ++i) bad = bad || bad_half2(h[i]);
+            bad = bad && here;
             // the UPK lanes of a key are one warp's (8 or 32 consecutive lanes)
             const unsigned bm = __ballot_sync(0xffffffffu, bad) >> (UPK == 32 ? 0 : (lane / UPK) * UPK);
             const bool kbad = (bm & (UPK == 32 ? 0xffffffffu : (1u << (UPK & 31)) - 1u)) != 0;
-            if (kbad)
+            if (kbad || !here)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] = 0;
-            *reinterpret_cast<uint4*>(ks + swz<D * 2>(key, 2 * u)) = make_uint4(h[0], h[1], h[2], h[3]);
-            *reinterpret_cast<uint4*>(ks + swz<D * 2>(key, 2 * u + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-            if (u == 0) s_add[key] = row < 0 ? -INFINITY : (kbad ? __int_as_float(0x7fc00000) : 0.0f);
-            flagged = flagged || kbad || (row < 0 && slot < T.n_tot);
+            // (the upper half of the units stores its chunks in the other order: eight lanes, eight bank groups)
+            const int sw = (u >> 2) & 1;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *reinterpret_cast<uint4*>(ks + swz<D * 2>(key, 2 * u + sw)) = sw ? hi : lo;
+            *reinterpret_cast<uint4*>(ks + swz<D * 2>(key, 2 * u + 1 - sw)) = sw ? lo : hi;
+            if (u == 0) s_add[key] = !here ? -INFINITY : (kbad ? __int_as_float(0x7fc00000) : 0.0f);
+            flagged = flagged || kbad || (!here && slot < T.n_tot);
         }
+        have = copy_tile(t + 1);                 // (no pages past the last tile: nothing is copied)
+        fetch_pages(t + 2);
         flagged = __syncthreads_or(flagged);
 
         // ---- S = Q K^T for 16 rows and this warp's keys
@@ -414,24 +482,35 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
     float acc[CL];
 #pragma unroll
     for (int i = 0; i < CL; ++i) acc[i] = 0.0f;
-    for (int s = 0; s < S; ++s) {
-        const float ws = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);
-        if (ws == 0.0f) continue;
-        const uint16_t* src = p.part_o + ((part + s) * R + r) * D + lane * CL;
-        uint32_t v[CL / 2];
-        if constexpr (CL >= 8) {
+    constexpr int BS = 8;                        // splits whose loads fly together
+    for (int s0 = 0; s0 < S; s0 += BS) {
+        uint32_t v[BS][CL / 2];
+        float ws[BS];
 #pragma unroll
-            for (int i = 0; i < CL / 8; ++i)
-                *reinterpret_cast<uint4*>(v + 4 * i) = *(reinterpret_cast<const uint4*>(src) + i);
-        } else {
-            *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(src);
+        for (int j = 0; j < BS; ++j) {
+            const int s = s0 + j;
+            ws[j] = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);     // 0 past the last split
+#pragma unroll
+            for (int i = 0; i < CL / 2; ++i) v[j][i] = 0;
+            if (ws[j] != 0.0f) {                 // (an empty split's O was not written)
+                const uint16_t* src = p.part_o + ((part + s) * R + r) * D + lane * CL;
+                if constexpr (CL >= 8) {
+#pragma unroll
+                    for (int i = 0; i < CL / 8; ++i)
+                        *reinterpret_cast<uint4*>(v[j] + 4 * i) = *(reinterpret_cast<const uint4*>(src) + i);
+                } else {
+                    *reinterpret_cast<uint2*>(v[j]) = *reinterpret_cast<const uint2*>(src);
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < CL / 2; ++i) {
-            const float2 f = unpack_half2(v[i]);
-            acc[2 * i] += ws * f.x;
-            acc[2 * i + 1] += ws * f.y;
-        }
+        for (int j = 0; j < BS; ++j)
+#pragma unroll
+            for (int i = 0; i < CL / 2; ++i) {
+                const float2 f = unpack_half2(v[j][i]);
+                acc[2 * i] += ws[j] * f.x;
+                acc[2 * i + 1] += ws[j] * f.y;
+            }
     }
 #pragma unroll
     for (int i = 0; i < CL; ++i) acc[i] *= inv;

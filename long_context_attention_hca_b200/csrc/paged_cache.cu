@@ -387,13 +387,24 @@ page_compress_kernel(CompArgs a) {
     if (tail) {
         const int64_t t0 = max(ctx, end / M * M);
         const size_t toff = (static_cast<size_t>(b) * M) * D + ch;
-#pragma unroll 8
-        for (int64_t t = t0; t < end; ++t) {
-            const size_t from = static_cast<size_t>(q0 + t - ctx) * D + ch, to = toff + static_cast<size_t>(t % M) * D;
-            const uint32_t xv = *reinterpret_cast<const uint32_t*>(a.x + from);
-            const uint32_t gv = *reinterpret_cast<const uint32_t*>(a.gate + from);
-            *reinterpret_cast<uint32_t*>(a.tail_x + to) = xv;
-            *reinterpret_cast<uint32_t*>(a.tail_gate + to) = gv;
+        const int n = static_cast<int>(end - t0);            // < M
+        const size_t from = static_cast<size_t>(q0 + t0 - ctx) * D + ch;
+        const size_t to = toff + static_cast<size_t>(t0 % M) * D;
+        constexpr int TB = M < 16 ? M : 16;                  // rows whose loads fly together
+        for (int i0 = 0; i0 < n; i0 += TB) {
+            uint32_t xv[TB], gv[TB];
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                if (i0 + j < n) {
+                    xv[j] = *reinterpret_cast<const uint32_t*>(a.x + from + static_cast<size_t>(i0 + j) * D);
+                    gv[j] = *reinterpret_cast<const uint32_t*>(a.gate + from + static_cast<size_t>(i0 + j) * D);
+                }
+#pragma unroll
+            for (int j = 0; j < TB; ++j)
+                if (i0 + j < n) {
+                    *reinterpret_cast<uint32_t*>(a.tail_x + to + static_cast<size_t>(i0 + j) * D) = xv[j];
+                    *reinterpret_cast<uint32_t*>(a.tail_gate + to + static_cast<size_t>(i0 + j) * D) = gv[j];
+                }
         }
     }
 }

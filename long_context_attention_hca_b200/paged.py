@@ -45,6 +45,11 @@ _lib.paged_attn_window.argtypes = [_V, _I64, _I32, _I32, _V, _V, _I64, Layout, _
 _lib.paged_attn_window.restype = ctypes.c_int
 
 
+def _ok(t, dt, shape, dev):
+    """The usual case, decided in well under a microsecond."""
+    return t.dtype is dt and t.shape == shape and t.is_contiguous() and t.device == dev
+
+
 def _want(dev, *specs):
     """Each (tensor, dtype, shape, name): contiguous, on `dev`, of that dtype
     and shape (None: any extent)."""
@@ -71,20 +76,32 @@ def _on(dev):
     return _NONE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+# the current stream's handle without building a Stream object, where torch offers it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _st(dev, stream):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _raw_stream(dev.index)
     if stream.device != dev:
         raise ValueError(f"stream: must be of {dev}, is of {stream.device}")
     return stream.cuda_stream
 
 
+_LAYOUT = {(512, 64, 64): Layout(512, 64, 64), (128, 32, 32): Layout(128, 32, 32)}
+
+
+def _layout(layout):
+    return _LAYOUT.get(tuple(layout)) or Layout(*layout)
+
+
 def _entry_extras(extras, layout, dev):
     if extras is None:
         return None
-    if extras.norm_w is not None:
+    if extras.norm_w is not None and not _ok(extras.norm_w, _FLOAT, (layout[0],), dev):
         _want(dev, (extras.norm_w, _FLOAT, (layout[0],), "norm_w"))
-    if extras.inv_freq is not None:
+    if extras.inv_freq is not None and not _ok(extras.inv_freq, _FLOAT, (layout[1] // 2,), dev):
         _want(dev, (extras.inv_freq, _FLOAT, (layout[1] // 2,), "inv_freq"))
     return ctypes.byref(extras.c_struct())
 
@@ -109,6 +126,10 @@ class PagePlan:
 
     def check(self, dev, B=None):
         n = self.slot.shape[0]
+        s = self.row_start
+        if (_ok(self.slot, _LONG, (n,), dev) and _ok(self.row_pos, _INT, (n,), dev) and _ok(self.row_req, _INT, (n,), dev)
+                and _ok(s, _INT, (s.shape[0] if B is None else B + 1,), dev) and s.shape[0] > 0):
+            return
         _want(dev, (self.row_start, _INT, (None if B is None else B + 1,), "plan.row_start"),
               (self.row_req, _INT, (n,), "plan.row_req"), (self.row_pos, _INT, (n,), "plan.row_pos"),
               (self.slot, _LONG, (n,), "plan.slot"))
@@ -130,15 +151,19 @@ def kv_page_plan(ctx_len, new_len, m: int, page_size: int, block_table, free_pag
             raise ValueError("kv_page_plan: give plan or max_rows")
         with _NONE if stream is None else torch.cuda.stream(stream):
             plan = PagePlan.empty(B, max_rows, dev)
-    _want(dev, (ctx_len, _INT, (B,), "ctx_len"), (new_len, _INT, (B,), "new_len"),
-          (block_table, _INT, (B, None), "block_table"), (free_pages, _INT, (None,), "free_pages"),
-          (free_count, _INT, (1,), "free_count"), (plan.missing, _INT, (1,), "plan.missing"),
-          (plan.free_left, _INT, (1,), "plan.free_left"))
+    width, n_free = block_table.shape[-1], free_pages.shape[0]
+    if not (_ok(ctx_len, _INT, (B,), dev) and _ok(new_len, _INT, (B,), dev) and _ok(block_table, _INT, (B, width), dev)
+            and _ok(free_pages, _INT, (n_free,), dev) and _ok(free_count, _INT, (1,), dev)
+            and _ok(plan.missing, _INT, (1,), dev) and _ok(plan.free_left, _INT, (1,), dev)):
+        _want(dev, (ctx_len, _INT, (B,), "ctx_len"), (new_len, _INT, (B,), "new_len"),
+              (block_table, _INT, (B, None), "block_table"), (free_pages, _INT, (None,), "free_pages"),
+              (free_count, _INT, (1,), "free_count"), (plan.missing, _INT, (1,), "plan.missing"),
+              (plan.free_left, _INT, (1,), "plan.free_left"))
     plan.check(dev, B)
     with _on(dev):
         _check(_lib.kv_page_plan(ctx_len.data_ptr(), new_len.data_ptr(), B, m, page_size, block_table.data_ptr(),
-                                 block_table.shape[1], free_pages.data_ptr(), free_count.data_ptr(),
-                                 free_pages.shape[0], plan.slot.shape[0], plan.row_start.data_ptr(),
+                                 width, free_pages.data_ptr(), free_count.data_ptr(),
+                                 n_free, plan.slot.shape[0], plan.row_start.data_ptr(),
                                  plan.row_req.data_ptr(), plan.row_pos.data_ptr(), plan.slot.data_ptr(),
                                  plan.missing.data_ptr(), plan.free_left.data_ptr(), _st(dev, stream)), "kv_page_plan")
     return plan
@@ -150,15 +175,17 @@ def kv_page_store(x, plan: PagePlan, pages, layout, extras=None, stream=None):
     EntryExtras (RMSNorm, RoPE at each token's position) or None (a copy)."""
     dev = _device(x, "x")
     n, d = x.shape[0], layout[0]
-    _want(dev, (x, _BF, (None, d), "x"), (pages, _BF, (None, None, d), "pages"))
+    np_, ps = pages.shape[0], pages.shape[-2]
+    if not (_ok(x, _BF, (n, d), dev) and _ok(pages, _BF, (np_, ps, d), dev)):
+        _want(dev, (x, _BF, (None, d), "x"), (pages, _BF, (None, None, d), "pages"))
     plan.check(dev)
     if n > plan.slot.shape[0]:
         raise ValueError("x: more rows than the plan holds")
     with _on(dev):
         _check(_lib.kv_page_store(x.data_ptr(), n, plan.row_start.data_ptr() + 4 * (plan.row_start.shape[0] - 1),
-                                  plan.row_pos.data_ptr(), plan.slot.data_ptr(), Layout(*layout),
-                                  _entry_extras(extras, layout, dev), pages.data_ptr(),
-                                  pages.shape[0] * pages.shape[1], _st(dev, stream)), "kv_page_store")
+                                  plan.row_pos.data_ptr(), plan.slot.data_ptr(), _layout(layout),
+                                  _entry_extras(extras, layout, dev), pages.data_ptr(), np_ * ps, _st(dev, stream)),
+               "kv_page_store")
     return pages
 
 
@@ -173,10 +200,14 @@ def kv_page_compress(x, gate, pos_bias, row_start, ctx_len, plan: PagePlan, tail
     dev = _device(x, "x")
     d, B, m = cache.layout[0], ctx_len.shape[0], pos_bias.shape[0]
     n = x.shape[0]
-    _want(dev, (x, _BF, (n, d), "x"), (gate, _BF, (n, d), "gate"), (pos_bias, _FLOAT, (m, d), "pos_bias"),
-          (row_start, _INT, (B + 1,), "row_start"), (ctx_len, _INT, (B,), "ctx_len"),
-          (tail_x, _BF, (B, m, d), "tail_x"), (tail_gate, _BF, (B, m, d), "tail_gate"),
-          (cache.codes, torch.uint8, (None, None, None), "cache"))
+    if not (_ok(x, _BF, (n, d), dev) and _ok(gate, _BF, (n, d), dev) and _ok(pos_bias, _FLOAT, (m, d), dev)
+            and _ok(row_start, _INT, (B + 1,), dev) and _ok(ctx_len, _INT, (B,), dev)
+            and _ok(tail_x, _BF, (B, m, d), dev) and _ok(tail_gate, _BF, (B, m, d), dev)):
+        _want(dev, (x, _BF, (n, d), "x"), (gate, _BF, (n, d), "gate"), (pos_bias, _FLOAT, (m, d), "pos_bias"),
+              (row_start, _INT, (B + 1,), "row_start"), (ctx_len, _INT, (B,), "ctx_len"),
+              (tail_x, _BF, (B, m, d), "tail_x"), (tail_gate, _BF, (B, m, d), "tail_gate"))
+    if cache.codes.device != dev:
+        raise ValueError(f"cache: must be on {dev}")
     plan.check(dev, B)
     with _on(dev):
         _check(_lib.kv_page_compress(m, x.data_ptr(), gate.data_ptr(), n, row_start.data_ptr(), ctx_len.data_ptr(), B,
@@ -190,7 +221,7 @@ def kv_page_compress(x, gate, pos_bias, row_start, ctx_len, plan: PagePlan, tail
 def paged_attn_workspace_size(n_rows, B, H, layout, max_new, max_entries, W, n_first=0) -> int:
     """Bytes of ws for paged_attn_chunk (max_entries = entry table width x page
     size, n_first = 0) and paged_attn_window (max_entries = 0)."""
-    return int(_lib.paged_attn_workspace_size(n_rows, B, H, Layout(*layout), max_new or 0, max_entries, W, n_first))
+    return int(_lib.paged_attn_workspace_size(n_rows, B, H, _layout(layout), max_new or 0, max_entries, W, n_first))
 
 
 def _attn_extras(extras, H, layout, dev):
@@ -198,7 +229,7 @@ def _attn_extras(extras, H, layout, dev):
         return None
     for t, shape, n in ((extras.q_norm_w, (layout[0],), "q_norm_w"), (extras.sink, (H,), "sink"),
                         (extras.inv_freq, (layout[1] // 2,), "inv_freq")):
-        if t is not None:
+        if t is not None and not _ok(t, _FLOAT, shape, dev):
             _want(dev, (t, _FLOAT, shape, n))
     return ctypes.byref(extras.c_struct())
 
@@ -207,36 +238,52 @@ def _attn(q, row_start, ctx_len, pages, token_table, W, scale, m, cache, entry_t
           extras):
     dev = _device(q, "q")
     N, H, d = q.shape
-    layout = LAYOUT_512 if d == 512 else LAYOUT_128
+    layout = LAYOUT_512 if d == 512 else LAYOUT_128        # (another d fails the check of q's shape)
     B = ctx_len.shape[0]
-    _want(dev, (q, _BF, (N, H, layout[0]), "q"), (row_start, _INT, (B + 1,), "row_start"),
-          (ctx_len, _INT, (B,), "ctx_len"), (pages, _BF, (None, None, d), "pages"),
-          (token_table, _INT, (B, None), "token_table"))
+    d = layout[0]
+    np_, ps, width = pages.shape[0], pages.shape[-2], token_table.shape[-1]
+    if not (_ok(q, _BF, (N, H, d), dev) and _ok(row_start, _INT, (B + 1,), dev) and _ok(ctx_len, _INT, (B,), dev)
+            and _ok(pages, _BF, (np_, ps, d), dev) and _ok(token_table, _INT, (B, width), dev)):
+        _want(dev, (q, _BF, (N, H, d), "q"), (row_start, _INT, (B + 1,), "row_start"), (ctx_len, _INT, (B,), "ctx_len"),
+              (pages, _BF, (None, None, d), "pages"), (token_table, _INT, (B, None), "token_table"))
     max_entries = 0
     if cache is not None:
         if cache.layout[0] != d:
             raise ValueError("cache: its layout does not match q")
-        _want(dev, (cache.codes, torch.uint8, (None, None, None), "cache"), (entry_table, _INT, (B, None), "entry_table"))
-        max_entries = entry_table.shape[1] * cache.capacity
+        if cache.codes.device != dev:
+            raise ValueError(f"cache: must be on {dev}")
+        e_width = entry_table.shape[-1]
+        if not _ok(entry_table, _INT, (B, e_width), dev):
+            _want(dev, (entry_table, _INT, (B, None), "entry_table"))
+        max_entries = e_width * cache.capacity
     max_new = int(max_new or 0)
-    lay = Layout(*layout)
-    with _on(dev):
-        need = int(_lib.paged_attn_workspace_size(N, B, H, lay, max_new, max_entries, W, n_first))
-    # what is allocated here belongs to the stream that writes it
-    with _NONE if stream is None else torch.cuda.stream(stream):
-        if out is None:
-            out = torch.empty_like(q)
-        if need and ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _want(dev, (out, _BF, (N, H, d), "out"))
-    if ws is not None:
-        _want(dev, (ws, torch.uint8, (None,), "ws"))
-    wp, wn = (ws.data_ptr(), ws.shape[0]) if need else (None, 0)
-    tmap = PageMapStruct(token_table.data_ptr(), token_table.shape[1], pages.shape[1], pages.shape[0])
+    lay = _LAYOUT[layout]
     ex = _attn_extras(extras, H, layout, dev)
     with _on(dev):
+        need = _lib.paged_attn_workspace_size(N, B, H, lay, max_new, max_entries, W, n_first)
+        # what is allocated here belongs to the stream that writes it
+        if stream is None:
+            if out is None:
+                out = torch.empty_like(q)
+            if need and ws is None:
+                ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        else:
+            with torch.cuda.stream(stream):
+                if out is None:
+                    out = torch.empty_like(q)
+                if need and ws is None:
+                    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        if not _ok(out, _BF, (N, H, d), dev):
+            _want(dev, (out, _BF, (N, H, d), "out"))
+        wp, wn = None, 0
+        if ws is not None:
+            wn = ws.shape[0]
+            if not _ok(ws, torch.uint8, (wn,), dev):
+                _want(dev, (ws, torch.uint8, (None,), "ws"))
+            wp = ws.data_ptr()
+        tmap = PageMapStruct(token_table.data_ptr(), width, ps, np_)
         if cache is not None:
-            emap = PageMapStruct(entry_table.data_ptr(), entry_table.shape[1], cache.capacity, cache.B)
+            emap = PageMapStruct(entry_table.data_ptr(), e_width, cache.capacity, cache.B)
             _check(_lib.paged_attn_chunk(q.data_ptr(), N, H, B, row_start.data_ptr(), ctx_len.data_ptr(), max_new, m, lay,
                                          cache.c_struct, emap, pages.data_ptr(), tmap, W, scale, ex, out.data_ptr(), wp,
                                          wn, _st(dev, stream)), "paged_attn_chunk")
