@@ -53,11 +53,15 @@ struct Rows {
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" :: "r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 
 // row-major fp16 tile, 16-byte chunks XOR-swizzled by row (conflict-free ldmatrix)
 template <int W2>
@@ -93,6 +97,7 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     float* s_sc = reinterpret_cast<float*>(raw + C::RAW_BYTES);      // [key][8]
     __shared__ float s_max[8][16];               // [warp][row of its group]
     __shared__ float s_l[8][16];
+    __shared__ int64_t s_row[2][TK];             // [tile parity]: a key's row of its pool, -1: not visible
     __shared__ float s_add[TK];                  // -inf: no such key; NaN: the key holds a non-finite value
     const uint32_t qa = static_cast<uint32_t>(__cvta_generic_to_shared(qs));
     const uint32_t ka = static_cast<uint32_t>(__cvta_generic_to_shared(ks));
@@ -107,65 +112,68 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     const int t_begin = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.n_splits);
     const int t_end = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.n_splits);
 
-    // ---- keys: a thread copies 16-dim unit u of keys kr + KPP k as stored (cp.async), and later converts just what it
-    // copied itself (no barrier in between).  The copies of a tile fly while the tile before is computed, its page
-    // numbers one tile ahead of that.
-    constexpr int UPK = D / 16;                  // 16-dim units of a key
-    constexpr int KPP = 256 / UPK;               // keys per pass
-    constexpr int NP = TK / KPP;                 // passes of a tile
-    const int u = tid % UPK, kr = tid / UPK, d0 = u * 16;
+    // ---- queries as stored, into the key buffer (not in use yet); a lane copies what it will convert
+    constexpr int CL = D / 32;                   // consecutive dims of a lane
     const uint32_t raw_a = static_cast<uint32_t>(__cvta_generic_to_shared(raw));
     const uint32_t sc_a = static_cast<uint32_t>(__cvta_generic_to_shared(s_sc));
-    int32_t page[NP];                            // page number of the keys of the tile to copy next
-    auto slot_token = [&](int slot) -> uint32_t {
-        const int j = slot - T.n_e;
-        return static_cast<uint32_t>(j < T.n_f ? j : T.w_lo + (j - T.n_f));
-    };
-    auto fetch_pages = [&](int t) {
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int slot = t * TK + k * KPP + kr;
-            page[k] = -1;
+#pragma unroll 2
+    for (int r = warp; r < T.rows; r += 8) {
+        const uint16_t* src = p.q + (T.row0 + r) * D + lane * CL;
+        if constexpr (CL >= 8) {
+            cp16(ka + r * (D * 2) + lane * 32, src);
+            cp16(ka + r * (D * 2) + lane * 32 + 16, src + 8);
+        } else {
+            cp8(ka + r * (D * 2) + lane * 8, src);
+        }
+    }
+    cp_commit();
+
+    // ---- keys: 64 threads look up the pool rows of a tile's keys, one tile ahead of the copies; a thread copies
+    // 16-dim unit u of keys kr + KPP k as stored (cp.async), and later converts just what it copied itself, so that
+    // the copies of a tile fly while the tile before is computed.  The loops stay rolled: a CTA runs through them a
+    // few times only, and straight-line code would wait for its own instructions (a convert phase of 64 keys took
+    // 12K clocks the first time and 7K later when unrolled, with the lookups in every lane).
+    constexpr int UPK = D / 16;                  // 16-dim units of a key
+    constexpr int KPP = 256 / UPK;               // keys per pass
+    const int u = tid % UPK, kr = tid / UPK, d0 = u * 16;
+    auto look_up = [&](int t) {
+        if (tid < TK) {
+            const int slot = t * TK + tid;
+            int64_t row = -1;
             if (t < t_end && slot < T.n_tot) {
-                const bool ent = slot < T.n_e;
-                const uint32_t i = ent ? static_cast<uint32_t>(slot) : slot_token(slot);
-                const uint32_t c = i / (ent ? p.e_size : p.t_size), w = ent ? p.e_width : p.t_width;
-                if (c < w) page[k] = __ldg((ent ? p.e_table : p.t_table) + static_cast<size_t>(T.b) * w + c);
+                if (slot < T.n_e) {
+                    row = entry_row(p, T.b, static_cast<uint32_t>(slot));
+                } else {
+                    const int j = slot - T.n_e;
+                    row = token_row(p, T.b, static_cast<uint32_t>(j < T.n_f ? j : T.w_lo + (j - T.n_f)));
+                }
             }
+            s_row[t & 1][tid] = row;
         }
     };
-    // bit k: key k of the thread exists (a page inside the pool)
-    auto copy_tile = [&](int t) -> unsigned {
-        unsigned have = 0;
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int key = k * KPP + kr, slot = t * TK + key;
-            const bool ent = slot < T.n_e;
-            if (page[k] < 0 || page[k] >= (ent ? p.e_pages : p.t_pages)) continue;
-            have |= 1u << k;
-            if (ent) {
-                const int64_t row = static_cast<int64_t>(page[k]) * p.e_size + static_cast<uint32_t>(slot) % p.e_size;
-                if (d0 < C::DN) {
-                    cp16(raw_a + key * (D * 2) + u * 32, p.codes + row * C::DN + d0);
-                    if (u % (C::G / 16) == 0) cp4(sc_a + (key * 8 + u / (C::G / 16)) * 4, p.scales + row * (C::DN / C::G) + u / (C::G / 16));
-                } else {
-                    const uint16_t* src = p.rope + row * C::DR + (d0 - C::DN);
-                    cp16(raw_a + key * (D * 2) + u * 32, src);
-                    cp16(raw_a + key * (D * 2) + u * 32 + 16, src + 8);
-                }
+    auto copy_tile = [&](int t) {
+#pragma unroll 2
+        for (int key = kr; key < TK; key += KPP) {
+            const int64_t row = s_row[t & 1][key];
+            if (row < 0) continue;
+            const uint32_t dst = raw_a + key * (D * 2) + u * 32;
+            const void* src;
+            if (t * TK + key >= T.n_e) {
+                src = p.tok + row * D + d0;
+            } else if (d0 < C::DN) {
+                cp16(dst, p.codes + row * C::DN + d0);
+                if (u % (C::G / 16) == 0) cp4(sc_a + (key * 8 + u / (C::G / 16)) * 4, p.scales + row * (C::DN / C::G) + u / (C::G / 16));
+                continue;
             } else {
-                const int64_t row = static_cast<int64_t>(page[k]) * p.t_size + slot_token(slot) % p.t_size;
-                const uint16_t* src = p.tok + row * D + d0;
-                cp16(raw_a + key * (D * 2) + u * 32, src);
-                cp16(raw_a + key * (D * 2) + u * 32 + 16, src + 8);
+                src = p.rope + row * C::DR + (d0 - C::DN);
             }
+            cp16(dst, src);
+            cp16(dst + 16, static_cast<const char*>(src) + 16);
         }
         cp_commit();
-        return have;
     };
-    fetch_pages(t_begin);
-    unsigned have = copy_tile(t_begin);
-    fetch_pages(t_begin + 1);
+    look_up(t_begin);
+    look_up(t_begin + 1);
 
     // ---- queries -> fp16 (rows past the last are zero); RMSNorm and RoPE in fp32
     if (p.inv_freq) {
@@ -175,30 +183,24 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
             if (r == 0 || (T.r0 + r) % p.H == 0)
                 s_cs[w] = rope_cs(p.inv_freq, w % (C::DR / 2), T.ctx + (T.r0 + r) / p.H);
         }
-        __syncthreads();
     }
-    constexpr int CL = D / 32;                   // consecutive dims of a lane
-    uint32_t qv[R / 8][CL / 2];                  // every load in flight before the first use
+    __syncthreads();                             // the pool rows and the RoPE table
+    copy_tile(t_begin);
+    cp_wait<1>();                                // this lane's query parts
+#pragma unroll 1
+    for (int r = warp; r < R; r += 8) {
+        uint32_t v[CL / 2];
 #pragma unroll
-    for (int k = 0; k < R / 8; ++k) {
-        const int r = warp + 8 * k;
-#pragma unroll
-        for (int i = 0; i < CL / 2; ++i) qv[k][i] = 0;
+        for (int i = 0; i < CL / 2; ++i) v[i] = 0;
         if (r < T.rows) {
-            const uint16_t* src = p.q + (T.row0 + r) * D + lane * CL;
             if constexpr (CL >= 8) {
 #pragma unroll
                 for (int i = 0; i < CL / 8; ++i)
-                    *reinterpret_cast<uint4*>(qv[k] + 4 * i) = __ldg(reinterpret_cast<const uint4*>(src) + i);
+                    *reinterpret_cast<uint4*>(v + 4 * i) = *reinterpret_cast<const uint4*>(ks + r * (D * 2) + lane * 32 + i * 16);
             } else {
-                *reinterpret_cast<uint2*>(qv[k]) = __ldg(reinterpret_cast<const uint2*>(src));
+                *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(ks + r * (D * 2) + lane * 8);
             }
         }
-    }
-#pragma unroll
-    for (int k = 0; k < R / 8; ++k) {
-        const int r = warp + 8 * k;
-        uint32_t (&v)[CL / 2] = qv[k];
         float f[CL];
 #pragma unroll
         for (int i = 0; i < CL / 2; ++i) {
@@ -251,35 +253,24 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.0f, 0.0f};
 
     for (int t = t_begin; t < t_end; ++t) {
-        cp_wait();
+        cp_wait<0>();
         __syncthreads();                         // the last tile's keys and P are read
         bool flagged = false;
-#pragma unroll
-        for (int k = 0; k < NP; ++k) {
-            const int key = k * KPP + kr, slot = t * TK + key;
-            const bool here = (have >> k) & 1u;
+#pragma unroll 2
+        for (int key = kr; key < TK; key += KPP) {
+            const int slot = t * TK + key;
+            const bool here = s_row[t & 1][key] >= 0;
             uint32_t h[8];
             const uint4 r0 = *reinterpret_cast<const uint4*>(raw + key * (D * 2) + u * 32);
             if (slot < T.n_e && d0 < C::DN) {
-                const float sc = s_sc[key * 8 + u / (C::G / 16)];
-                const uint32_t cw[4] = {r0.x, r0.y, r0.z, r0.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] & 0xFFFFu)));
-                    const float2 b = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] >> 16)));
-                    h[2 * i] = pack_half2(a.x * sc, a.y * sc);
-                    h[2 * i + 1] = pack_half2(b.x * sc, b.y * sc);
-                }
+                dequant16(r0, s_sc[key * 8 + u / (C::G / 16)], h);
             } else {
                 const uint4 r1 = *reinterpret_cast<const uint4*>(raw + key * (D * 2) + u * 32 + 16);
                 const uint32_t w[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
             }
-            bool bad = false;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) bad = bad || bad_half2(h[i]);
-            bad = bad && here;
+            const bool bad = here && any_bad16(h);
             // the UPK lanes of a key are one warp's (8 or 32 consecutive lanes)
             const unsigned bm = __ballot_sync(0xffffffffu, bad) >> (UPK == 32 ? 0 : (lane / UPK) * UPK);
             const bool kbad = (bm & (UPK == 32 ? 0xffffffffu : (1u << (UPK & 31)) - 1u)) != 0;
@@ -294,9 +285,9 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
             if (u == 0) s_add[key] = !here ? -INFINITY : (kbad ? __int_as_float(0x7fc00000) : 0.0f);
             flagged = flagged || kbad || (!here && slot < T.n_tot);
         }
-        have = copy_tile(t + 1);                 // (no pages past the last tile: nothing is copied)
-        fetch_pages(t + 2);
+        copy_tile(t + 1);                        // (no rows past the last tile: nothing is copied)
         flagged = __syncthreads_or(flagged);
+        look_up(t + 2);
 
         // ---- S = Q K^T for 16 rows and this warp's keys
         float s[C::NT][4];
@@ -418,24 +409,35 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
         ml[0] = m_r[0]; ml[8] = m_r[1];
         ml[R] = l_r[0]; ml[R + 8] = l_r[1];
     }
-#pragma unroll
-    for (int j = 0; j < C::NO; ++j) {
-        const int d = kg * C::DW + j * 8 + q4 * 2;
+    const int r0 = rg * 16 + g8;
+    if (p.n_splits > 1) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int r = rg * 16 + g8 + 8 * i;
+            if (r0 + 8 * i >= T.rows) continue;
+            uint16_t* dst = p.part_o + (part * R + r0 + 8 * i) * D + kg * C::DW + q4 * 2;
+#pragma unroll
+            for (int j = 0; j < C::NO; ++j)
+                *reinterpret_cast<uint32_t*>(dst + j * 8) = pack_half2(o[j][2 * i] * inv[i], o[j][2 * i + 1] * inv[i]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = r0 + 8 * i;
             if (r >= T.rows) continue;
-            float x = o[j][2 * i] * inv[i], y = o[j][2 * i + 1] * inv[i];
-            if (p.n_splits > 1) {
-                *reinterpret_cast<uint32_t*>(p.part_o + (part * R + r) * D + d) = pack_half2(x, y);
-            } else {
+            const int h = (T.r0 + r) % p.H;
+            const float2* cs = s_cs + max(r - h, 0) * (C::DR / 2);
+            uint16_t* dst = p.out + (T.row0 + r) * D + kg * C::DW + q4 * 2;
+#pragma unroll
+            for (int j = 0; j < C::NO; ++j) {
+                const int d = kg * C::DW + j * 8 + q4 * 2;
+                float x = o[j][2 * i] * inv[i], y = o[j][2 * i + 1] * inv[i];
                 if (p.inv_freq && d >= C::DN) {
-                    const int h = (T.r0 + r) % p.H;
-                    const float2 cs = s_cs[max(r - h, 0) * (C::DR / 2) + (d - C::DN) / 2];
-                    const float x2 = x * cs.x + y * cs.y, y2 = y * cs.x - x * cs.y;
-                    x = x2; y = y2;
+                    const float2 c = cs[(d - C::DN) / 2];
+                    const float x2 = x * c.x + y * c.y;
+                    y = y * c.x - x * c.y;
+                    x = x2;
                 }
-                *reinterpret_cast<__nv_bfloat162*>(p.out + (T.row0 + r) * D + d) = __floats2bfloat162_rn(x, y);
+                *reinterpret_cast<__nv_bfloat162*>(dst + j * 8) = __floats2bfloat162_rn(x, y);
             }
         }
     }
@@ -443,26 +445,30 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
 
 // ---------------------------------------------------------------- combine
 // Joins a tile's splits: out = sum_s 2^(m_s - M) l_s o_s / (sum_s 2^(m_s - M)
-// l_s [+ sink]), o_s = O_s / l_s in fp16 (half the traffic of fp32; 2^-12
-// relative, an eighth of the output's bf16 step).  A warp per row, its lanes
-// over the dims; lanes 0..S-1 (twice for S > 32) hold the weights.
+// l_s [+ sink]), o_s = O_s / l_s in fp16 (half the traffic of fp32; 2^-11
+// relative, an eighth of the output's bf16 step).  Bound: the latency of the
+// loads, so four warps share a row: each takes every fourth split, its lanes
+// over the dims, eight splits' loads in flight; the four sums meet in shared
+// memory.  Lane s of every warp holds split s's weight (twice for S > 32).
 template <int D, int R>
 __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
     constexpr int DR = D == 512 ? 64 : 32, DN = D - DR, CL = D / 32;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float s_acc[8][CL][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
     pdl_wait();                                  // the partials are complete
     Tile T;
     if (!make_tile(p, blockIdx.x, R, T) || T.n_new >= p.min_chunk) return;
-    const int r = blockIdx.y * 8 + warp;
-    if (r >= T.rows) return;
+    const int r = blockIdx.y * 2 + (warp >> 2);
+    if (blockIdx.y * 2 >= T.rows) return;        // both rows of the block
+    const bool row = r < T.rows;
     const int S = p.n_splits;
     const int64_t part = static_cast<int64_t>(blockIdx.x) * S;
     float m[2], l[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const int s = lane + 32 * k;
-        m[k] = s < S ? p.part_ml[(part + s) * 2 * R + r] : -INFINITY;
-        l[k] = s < S ? p.part_ml[(part + s) * 2 * R + R + r] : 0.0f;
+        m[k] = row && s < S ? p.part_ml[(part + s) * 2 * R + r] : -INFINITY;
+        l[k] = row && s < S ? p.part_ml[(part + s) * 2 * R + R + r] : 0.0f;
     }
     float M = fmaxf(m[0], m[1]);
 #pragma unroll
@@ -476,20 +482,19 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
     }
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-    const int h = (T.r0 + r) % p.H;
-    if (p.sink && (M != -INFINITY || L != L)) L += ex2(__ldg(p.sink + h) * LOG2E - M);
-    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
     float acc[CL];
 #pragma unroll
     for (int i = 0; i < CL; ++i) acc[i] = 0.0f;
     constexpr int BS = 8;                        // splits whose loads fly together
-    for (int s0 = 0; s0 < S; s0 += BS) {
+#pragma unroll 1
+    for (int s0 = quarter; s0 < S; s0 += 4 * BS) {
         uint32_t v[BS][CL / 2];
         float ws[BS];
 #pragma unroll
         for (int j = 0; j < BS; ++j) {
-            const int s = s0 + j;
-            ws[j] = __shfl_sync(0xffffffffu, s < 32 ? w[0] : w[1], s & 31);     // 0 past the last split
+            const int s = s0 + 4 * j;
+            const float a = __shfl_sync(0xffffffffu, w[0], s & 31), b = __shfl_sync(0xffffffffu, w[1], s & 31);
+            ws[j] = s < S ? (s < 32 ? a : b) : 0.0f;
 #pragma unroll
             for (int i = 0; i < CL / 2; ++i) v[j][i] = 0;
             if (ws[j] != 0.0f) {                 // (an empty split's O was not written)
@@ -513,7 +518,15 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
             }
     }
 #pragma unroll
-    for (int i = 0; i < CL; ++i) acc[i] *= inv;
+    for (int i = 0; i < CL; ++i) s_acc[warp][i][lane] = acc[i];
+    __syncthreads();
+    if (quarter != 0 || !row) return;
+    const int h = (T.r0 + r) % p.H;
+    if (p.sink && (M != -INFINITY || L != L)) L += ex2(__ldg(p.sink + h) * LOG2E - M);
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int i = 0; i < CL; ++i)
+        acc[i] = (acc[i] + s_acc[warp + 1][i][lane] + s_acc[warp + 2][i][lane] + s_acc[warp + 3][i][lane]) * inv;
     if (p.inv_freq && lane * CL >= DN) {
         const int64_t pos = T.ctx + (T.r0 + r) / p.H;
 #pragma unroll
@@ -602,7 +615,7 @@ static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
     kern<<<dim3(static_cast<unsigned>(k.tiles), k.splits), 256, Rows<D, R>::SMEM, st>>>(p);
     HCA_CHECK_LAUNCH();
     if (k.splits > 1) {
-        e = launch_pdl(paged_combine_kernel<D, R>, dim3(static_cast<unsigned>(k.tiles), R / 8), dim3(256), 0, st, p);
+        e = launch_pdl(paged_combine_kernel<D, R>, dim3(static_cast<unsigned>(k.tiles), R / 2), dim3(256), 0, st, p);
         if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
         HCA_CHECK_LAUNCH();
     }

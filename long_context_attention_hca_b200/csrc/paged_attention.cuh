@@ -153,9 +153,44 @@ __device__ __forceinline__ int64_t token_row(const Params& p, int b, uint32_t t)
     return id >= 0 && id < p.t_pages ? id * p.t_size + t % p.t_size : -1;
 }
 
-// a pair of fp16 holds an infinity or a NaN
-__device__ __forceinline__ bool bad_half2(uint32_t h) {
-    return (h & 0x7C00u) == 0x7C00u || (h & 0x7C000000u) == 0x7C000000u;
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Whether any of these 16 fp16 values is an infinity or a NaN: x * 0 is then a
+// NaN and stays one in the sum, and +-0 otherwise.
+__device__ __forceinline__ bool any_bad16(const uint32_t (&h)[8]) {
+    uint32_t z = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(h[i]), "r"(0u));
+    return (z & 0x7FFF7FFFu) != 0;
+}
+
+// 16 FP8 codes x their scale -> fp16.  A scale in fp16's normal range is
+// rounded to fp16 (half a step, 2^-11) and each product once more (2^-11): one
+// conversion and one multiplication per pair, where products in fp32 take four
+// conversions per pair, at a quarter of the rate.  Any other scale: fp32
+// products, rounded once.
+__device__ __forceinline__ void dequant16(const uint4& cv, float sc, uint32_t (&h)[8]) {
+    const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
+    if (sc >= 6.103515625e-05f && sc <= 65504.0f) {
+        const uint32_t s2 = pack_half2(sc, sc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            h[2 * i] = hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] & 0xFFFFu)), s2);
+            h[2 * i + 1] = hmul2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] >> 16)), s2);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] & 0xFFFFu)));
+            const float2 b = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[i] >> 16)));
+            h[2 * i] = pack_half2(a.x * sc, a.y * sc);
+            h[2 * i + 1] = pack_half2(b.x * sc, b.y * sc);
+        }
+    }
 }
 
 // cos / sin of RoPE pair i at position t, fp32 out.  The angle t f_i is exact in

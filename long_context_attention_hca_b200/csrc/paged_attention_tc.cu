@@ -120,15 +120,7 @@ __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
         if (row >= 0) {
             if (d0 < DN) {
                 const uint4 cv = __ldg(reinterpret_cast<const uint4*>(p.codes + row * DN + d0));
-                const float sc = __ldg(p.scales + row * (DN / 64) + d0 / 64);
-                const uint32_t cw[4] = {cv.x, cv.y, cv.z, cv.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 a = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[k] & 0xFFFFu)));
-                    const float2 c = unpack_half2(e4m3x2_to_f16x2(static_cast<uint16_t>(cw[k] >> 16)));
-                    h[2 * k] = pack_half2(a.x * sc, a.y * sc);
-                    h[2 * k + 1] = pack_half2(c.x * sc, c.y * sc);
-                }
+                dequant16(cv, __ldg(p.scales + row * (DN / 64) + d0 / 64), h);
             } else {
                 const uint4* rp = reinterpret_cast<const uint4*>(p.rope + row * DR + (d0 - DN));
                 const uint4 a = __ldg(rp), c = __ldg(rp + 1);
@@ -152,10 +144,7 @@ __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
                 h[k] = pack_half2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
         }
     }
-    bool bad = false;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) bad = bad || bad_half2(h[k]);
-    bad = __any_sync(0xffffffffu, bad);
+    const bool bad = __any_sync(0xffffffffu, any_bad16(h));
     const uint32_t keep = bad ? 0u : 0xffffffffu;
     uint4* dst = reinterpret_cast<uint4*>(s.rows + g * D + d0);
     dst[0] = make_uint4(h[0] & keep, h[1] & keep, h[2] & keep, h[3] & keep);

@@ -3,16 +3,16 @@ and slot maps, token and entry stores (bit for bit), attention of ragged chunks
 and single tokens over pages, and steps of all of them together.
 
 Attention tolerance, per output element, from the roundings on the way (u16 =
-2^-11, half a step of fp16; ub = 2^-8, half a step of bf16): a key is rounded
-to fp16 once and the query once, so a logit is off by at most
-dl = scale * sum_i |q_i| |k_i| * (2 u16 + 2^-14), the last term covering the
-fp32 sum of d <= 512 products (512 * 2^-23 = 2^-14 where every addition
-truncates), plus 2^-12 for values below fp16's normal range (2^-25 off each);
-a weight is then off by a factor within e^(+-2 dl) and P by u16 more, the
-values by u16, a split's partial by u16: |error| <= (e^(2 dl) - 1 + 4 u16) *
-sum_j p_j |v_j| + ub |o|.  That is a worst case; the mean is held to what the
-workloads are held to: sum |a - b| / sum |b| <= 1e-3 for the arithmetic plus
-2^-9, the mean of a bf16 rounding (half of its largest).
+2^-11, half a step of fp16; ub = 2^-8, half a step of bf16): an entry's scale is
+rounded to fp16 and each product with a code once more, the query once, so a
+logit is off by at most dl = scale * sum_i |q_i| |k_i| * (3 u16 + 2^-14), the
+last term covering the fp32 sum of d <= 512 products (512 * 2^-23 = 2^-14 where
+every addition truncates), plus 2^-12 for values below fp16's normal range
+(2^-25 off each); a weight is then off by a factor within e^(+-2 dl) and P by
+u16 more, the values by 2 u16, a split's partial by u16: |error| <= (e^(2 dl) -
+1 + 4 u16) * sum_j p_j |v_j| + ub |o|.  That is a worst case; the mean is held
+to what the workloads are held to: sum |a - b| / sum |b| <= 1e-3 for the
+arithmetic plus 2^-9, the mean of a bf16 rounding (half of its largest).
 """
 import numpy as np
 import pytest
@@ -319,7 +319,7 @@ class Case:
                     top = np.maximum(top, self.kw["sink"][:, None])
                 w = np.exp(lg - top)
                 w /= w.sum(1, keepdims=True) + (np.exp(self.kw["sink"][:, None] - top) if self.extras else 0)
-                dl = self.scale * (np.abs(q) @ np.abs(k).T).max(1, keepdims=True) * (2 * U16 + 2.0 ** -14) + 2.0 ** -12
+                dl = self.scale * (np.abs(q) @ np.abs(k).T).max(1, keepdims=True) * (3 * U16 + 2.0 ** -14) + 2.0 ** -12
                 pv = w @ np.abs(k)
                 if self.extras:                          # the rotation back mixes a pair's errors
                     pr = pv[:, d - dr:]
