@@ -18,7 +18,7 @@ namespace paged {
 
 int64_t tc_stage_rows(int64_t n_rows, int B, int64_t max_entries, int W, int n_first);
 size_t tc_stage_bytes(int64_t rows);
-int tc_chunk_launch(const Params& p, int64_t max_entries, void* ws, cudaStream_t st);
+int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* ws, cudaStream_t st);
 
 // ---------------------------------------------------------------- row kernel
 // One CTA = one tile of R rows (tokens x heads, flattened inside a request) and
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
     const int split = blockIdx.y;
 
     Tile T;
-    if (!make_tile(p, blockIdx.x, R, T) || T.n_new >= p.min_chunk) return;
+    if (!make_tile(p, blockIdx.x, R, T)) return;
     const int n_tiles = (T.n_tot + TK - 1) / TK;
     const int t_begin = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.n_splits);
     const int t_end = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.n_splits);
@@ -457,7 +457,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3;
     pdl_wait();                                  // the partials are complete
     Tile T;
-    if (!make_tile(p, blockIdx.x, R, T) || T.n_new >= p.min_chunk) return;
+    if (!make_tile(p, blockIdx.x, R, T)) return;
     const int r = blockIdx.y * 2 + (warp >> 2);
     if (blockIdx.y * 2 >= T.rows) return;        // both rows of the block
     const bool row = r < T.rows;
@@ -553,57 +553,62 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
 }
 
 // ---------------------------------------------------------------- host side
-// A request goes to the chunk kernel when its rows fill two CTA pairs.
-constexpr int CHUNK_ROWS = 256;
-// Staged keys take 1 KB each: at most 2 GB of workspace, beyond that (64
-// requests whose tables reach 4M tokens, say) every request is the row kernel's.
+// Staged keys take 1 KB each: at most 2 GB of workspace; beyond that (64
+// requests whose entry tables reach 4M tokens, say) the row kernel serves d =
+// 512 too, several times slower.
 constexpr int64_t MAX_STAGE_ROWS = 2ll << 20;
+constexpr int PAIR_ROWS = 128;
 
-// Rows of a tile: 16 when no request can fill more (a small head count at
-// decode), else 64.
+// Rows of a row kernel's tile: 16 when no request can fill more (a small head
+// count at decode), else 64.
 inline int tile_rows(int64_t max_new, int H) { return max_new * H <= 16 ? 16 : 64; }
 inline int64_t tile_count(int64_t n_rows, int H, int B, int R) { return n_rows * H / R + B; }
 
-// Splits: enough CTAs for every SM when the tiles alone are too few, but at
-// least two key tiles for each (max_keys: the longest key list there can be).
-inline int split_count(int64_t tiles, int64_t max_keys) {
-    int64_t s = sm_count() / (tiles > 0 ? tiles : 1);
-    const int64_t by_len = ceil_div(ceil_div(max_keys, TK), 2);
+// Splits: enough work for every SM (pair) when the tiles alone are too few, but
+// at least min_tiles key tiles for each (max_keys: the longest key list there
+// can be).
+inline int split_count(int64_t slots, int64_t tiles, int64_t max_keys, int tile_keys, int min_tiles) {
+    int64_t s = slots / (tiles > 0 ? tiles : 1);
+    const int64_t by_len = ceil_div(ceil_div(max_keys, tile_keys), min_tiles);
     if (s > by_len) s = by_len;
     if (s > MAX_SPLITS) s = MAX_SPLITS;
     return s < 1 ? 1 : static_cast<int>(s);
 }
 
-// chunk: requests with at least this many new tokens go to the chunk kernel
-// (0: none do), the others to the row kernel, tiles_per_req tiles each.
-struct Plan { int R, splits, tiles_per_req, chunk; int64_t tiles; size_t stage_bytes; };
+struct Plan { bool pairs; int R, splits; int64_t tiles; size_t stage_bytes; };
 
 static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int64_t max_entries, int W, int n_first) {
     Plan k = {};
     // the longest key list of a tile: entries, first tokens, the window and the tile's own tokens
     const int64_t max_keys = max_entries + W + n_first + 64;
     const int64_t stage_rows = tc_stage_rows(n_rows, B, max_entries, W, n_first);
-    const int chunk = (CHUNK_ROWS + H - 1) / H < 2 ? 2 : (CHUNK_ROWS + H - 1) / H;
     const int64_t reqs = n_rows < B ? n_rows : B;      // requests that can have a new token
-    if (D == 512 && max_new >= chunk && stage_rows <= MAX_STAGE_ROWS) {
-        k.chunk = chunk;
-        k.stage_bytes = tc_stage_bytes(stage_rows);
-        k.R = 64;
-        k.tiles_per_req = (static_cast<int64_t>(chunk - 1) * H + k.R - 1) / k.R;
-        k.tiles = static_cast<int64_t>(B) * k.tiles_per_req;
-        k.splits = split_count(reqs, max_keys);
-        return k;
-    }
-    k.R = tile_rows(max_new, H);
+    k.pairs = D == 512 && stage_rows <= MAX_STAGE_ROWS;
+    k.R = k.pairs ? PAIR_ROWS : (D == 512 ? 64 : tile_rows(max_new, H));
     k.tiles = tile_count(n_rows, H, B, k.R);
     // tiles that can hold rows: one a request when no request fills more
-    k.splits = split_count(max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs, max_keys);
+    const int64_t busy = max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs;
+    if (k.pairs) {
+        k.stage_bytes = tc_stage_bytes(stage_rows);
+        k.splits = split_count(sm_count() / 2, busy, max_keys, 128, 2);
+    } else {
+        k.splits = split_count(sm_count(), busy, max_keys, TK, 2);
+    }
     return k;
 }
 
 static size_t part_bytes(const Plan& k, int D) {
     if (k.splits <= 1) return 0;
     return static_cast<size_t>(k.tiles) * k.splits * k.R * (static_cast<size_t>(D) * 2 + 2 * sizeof(float)) + 256;
+}
+
+template <int D, int R>
+static int launch_combine(const Params& p, const Plan& k, cudaStream_t st) {
+    if (k.splits <= 1) return HCA_OK;
+    const cudaError_t e = launch_pdl(paged_combine_kernel<D, R>, dim3(static_cast<unsigned>(k.tiles), R / 2), dim3(256), 0, st, p);
+    if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
+    HCA_CHECK_LAUNCH();
+    return HCA_OK;
 }
 
 template <int D, int R>
@@ -614,12 +619,7 @@ static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     kern<<<dim3(static_cast<unsigned>(k.tiles), k.splits), 256, Rows<D, R>::SMEM, st>>>(p);
     HCA_CHECK_LAUNCH();
-    if (k.splits > 1) {
-        e = launch_pdl(paged_combine_kernel<D, R>, dim3(static_cast<unsigned>(k.tiles), R / 2), dim3(256), 0, st, p);
-        if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
-        HCA_CHECK_LAUNCH();
-    }
-    return HCA_OK;
+    return launch_combine<D, R>(p, k, st);
 }
 
 }  // namespace paged
@@ -635,19 +635,15 @@ int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_entri
     const size_t need = k.stage_bytes + paged::part_bytes(k, D);
     if (need > 0 && (ws == nullptr || ws_bytes < need)) return HCA_ERR_WORKSPACE;
     p.n_splits = k.splits;
-    p.min_chunk = 0x7FFFFFFF;
-    if (k.chunk > 0) {
-        p.min_chunk = k.chunk;
-        const int rc = paged::tc_chunk_launch(p, max_entries, ws, st);
-        if (rc != HCA_OK) return rc;
-        p.tiles_per_req = k.tiles_per_req;
-    }
     if (k.splits > 1) {
         p.part_o = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(ws) + k.stage_bytes);
         p.part_ml = reinterpret_cast<float*>(p.part_o + static_cast<size_t>(k.tiles) * k.splits * k.R * D);
     }
-    if (D == 512)
-        return k.R == 16 ? paged::launch_rows<512, 16>(p, k, st) : paged::launch_rows<512, 64>(p, k, st);
+    if (k.pairs) {
+        const int rc = paged::tc_chunk_launch(p, k.tiles, max_entries, ws, st);
+        return rc == HCA_OK ? paged::launch_combine<512, paged::PAIR_ROWS>(p, k, st) : rc;
+    }
+    if (D == 512) return paged::launch_rows<512, 64>(p, k, st);
     return k.R == 16 ? paged::launch_rows<128, 16>(p, k, st) : paged::launch_rows<128, 64>(p, k, st);
 }
 

@@ -36,8 +36,6 @@ struct Params {
     int W, n_first;
     float scale_log2;
     int n_splits;
-    int min_chunk;              // requests with at least this many new tokens are the chunk kernel's
-    int tiles_per_req;          // 0, or the row kernel's tiles of a request (all have fewer new tokens than min_chunk)
     uint16_t* out;
     uint16_t* part_o;           // [tiles][splits][rows][D] fp16: O / l of the split
     float* part_ml;             // [tiles][splits][2][rows]: running max (base 2), l
@@ -95,13 +93,13 @@ __device__ __forceinline__ int64_t entries_before(const Params& p, int64_t pos) 
 
 // false: the tile has no rows here.  Called by whole warps.
 __device__ __forceinline__ bool make_tile(const Params& p, int64_t t, int R, Tile& T) {
-    const int b = p.tiles_per_req > 0 ? static_cast<int>(t / p.tiles_per_req) : find_tile_req(p, t, R);
+    const int b = find_tile_req(p, t, R);
     const int64_t s = p.row_start[b];
     int64_t e = p.row_start[b + 1];
     if (e > p.n_rows) e = p.n_rows;
     T.b = b;
     T.n_new = s < 0 || e < s ? 0 : static_cast<int>(e - s);
-    const int64_t r0 = (p.tiles_per_req > 0 ? t % p.tiles_per_req : t - tile0(p, b, R)) * R;
+    const int64_t r0 = (t - tile0(p, b, R)) * R;
     const int64_t left = static_cast<int64_t>(T.n_new) * p.H - r0;
     if (left <= 0 || r0 < 0) return false;
     T.r0 = static_cast<int>(r0);

@@ -1,12 +1,12 @@
-// paged_attention_tc.cu -- attention of prefill chunks over paged caches on the
-// sm_100a tensor cores, d = 512 (paged_attention.cu holds the attention rule
-// and the kernel for few rows).
+// paged_attention_tc.cu -- attention over paged caches on the sm_100a tensor
+// cores, d = 512 (paged_attention.cu holds the attention rule, the kernel for d
+// = 128 and the choice between the two).
 //
-// Two kernels.  The first writes each chunk request's keys once, dequantised to
-// fp16, into rows of the workspace (entries, then first tokens and window
-// tokens in position order): every one of the request's tokens reads them, so
-// that a page lookup, a dequantisation and a check for non-finite values per
-// key is paid once and the second kernel is fed by TMA alone.
+// Two kernels.  The first writes each request's keys once, dequantised to fp16,
+// into rows of the workspace (entries, then first tokens and window tokens in
+// position order): every one of the request's tokens reads them, so that a page
+// lookup, a dequantisation and a check for non-finite values per key is paid
+// once and the second kernel is fed by TMA alone.
 //
 // The second runs on CTA pairs (cta_group::2): 128 rows (tokens x heads,
 // flattened), 64 in each CTA, against tiles of 128 keys.
@@ -27,12 +27,19 @@
 // 16 KB pieces of one ring of 8, consumed in the order QK(0), QK(i + 1), PV(i),
 // ...: the softmax of tile i runs beside QK(i + 1).
 //
-// Warps: 0-7 query, softmax and output (two groups of four, tiles in turn; a
-// row of a tile is shared by two threads, one TMEM lane each), 8 TMA, 9 QK issue, 10 PV issue (the first CTA's only).
-// The online softmax is in base 2; O is rescaled only when a row's maximum
-// grows by more than 2^8 (P <= 2^8 in fp16).  Every wait is bounded: one that
-// gives up sets the device error word, the CTA's outputs become NaN, and the
-// pair still meets at the end.
+// The pairs are persistent: the grid is one pair per two SMs, and a pair takes
+// (tile, split of its keys) items from a counter until none is left, so that an
+// item's query load, first keys and first QK run beside the item before (its
+// last softmax, its output), and long and short items even out.  Splits are for
+// steps of few rows: their partial outputs are joined by the combine kernel.
+//
+// Warps: 0-7 softmax and output (two groups of four, tiles in turn; a row of a
+// tile is shared by two threads, one TMEM lane each), 8 TMA (in the first CTA
+// also the item counter), 9 QK issue, 10 PV issue (the first CTA's only), 11-14
+// query rows to fp16.  The online softmax is in base 2; O is rescaled only when
+// a row's maximum grows by more than 2^8 (P <= 2^8 in fp16).  Every wait is
+// bounded: one that gives up sets the device error word, the CTA's outputs
+// become NaN, and the pair still meets at the end.
 #include <cuda.h>
 
 #include "paged_attention.cuh"
@@ -54,7 +61,7 @@ constexpr int P_OFF = 65536;                 // 2 buffers of 2 column blocks (64
 constexpr int R_OFF = P_OFF + 2 * 16384;
 constexpr int CTRL_OFF = R_OFF + NSLOT * SLOT;
 constexpr int SMEM = 232448;                 // all that a CTA may have: the rest is Ctrl's
-constexpr int NSOFT = 8, NTHREADS = 11 * 32;
+constexpr int NSOFT = 8, NQ = 4, NTHREADS = (11 + NQ) * 32;
 constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 512;
 constexpr float GROW = 8.0f;                 // log2 units
 constexpr int DR = 64, DN = D - DR;
@@ -65,6 +72,8 @@ struct Stage {
     uint8_t* flags;             // [bound]: 1 not visible, 2 non-finite
     int64_t per_req;            // rows of a request besides its new tokens
     int64_t bound;              // rows of the workspace
+    int* next;                  // the item counter
+    int n_items;                // tiles x splits
 };
 
 // Request b's staged rows start at b per_req + row_start[b]: entries (padded
@@ -92,8 +101,9 @@ __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
     const int lane = threadIdx.x & 31;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     pdl_trigger();                              // the attention's prologue may start
+    if (g == 0 && lane == 0) *s.next = 0;
     if (g >= s.bound) return;
-    // largest b with b per_req + row_start[b] <= g
+    // largest b with b per_req + row_start[b] <= g, 32 candidates a round
     int lo = 0, hi = p.B;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
@@ -107,7 +117,7 @@ __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
     const int64_t st = p.row_start[b];
     const int64_t en = p.row_start[b + 1] < p.n_rows ? p.row_start[b + 1] : p.n_rows;
     const int n_new = st < 0 || en < st ? 0 : static_cast<int>(en - st);
-    if (n_new < p.min_chunk) return;
+    if (n_new == 0) return;
     const int64_t ctx = p.ctx[b] > 0 ? p.ctx[b] : 0;
     const Region r = region(p, s, b, ctx, n_new);
     int64_t i = g - r.base;
@@ -263,14 +273,51 @@ __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 8 * i - 4; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 8 * i + 4 : 8 * i + 8; }
 
 struct Ctrl {
-    uint64_t full[NSLOT], empty[NSLOT], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, drain;
+    uint64_t full[NSLOT], empty[NSLOT], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free;
+    uint64_t item_full[2], item_free[2], drain;
     float mx[2][2][ROWS];       // [group][key half][row]: a tile's largest raw logit
-    float m[2][ROWS];           // [tile parity][row]: the running maximum (base 2) after the tile
+    float m[2][ROWS];           // [tile parity]: the running maximum (base 2) after the tile
     float l[4][ROWS];
+    int item[2], soft_item;
     uint32_t tmem;
     int abort_flag;
 };
 static_assert(CTRL_OFF + sizeof(Ctrl) <= SMEM, "shared memory");
+// warps that take an item from the mailbox: softmax (one for all), QK, PV and the query warps of the first CTA;
+// softmax, TMA and the query warps of the second
+constexpr int TAKERS = 3 + NQ + 2 + NQ;
+
+// One item: a tile's rows and the key tiles [k0, k0 + n) of its split.
+struct Item {
+    Tile T;
+    int split, k0, n;
+    int h_e, h_f, n_half;       // half tiles of 64 staged rows: entries, first tokens, all
+    int64_t ent0, tok0, win0;   // staged rows of the first entry, first token, first window token
+};
+
+__device__ __forceinline__ bool make_item(const Params& p, const Stage& s, int item, Item& I) {
+    const int t = item / p.n_splits;
+    I.split = item - t * p.n_splits;
+    if (!make_tile(p, t, PAIR, I.T)) return false;
+    const Region rg = region(p, s, I.T.b, I.T.ctx, I.T.n_new);
+    I.h_e = (I.T.n_e + HALF - 1) / HALF;
+    I.h_f = (I.T.n_f + HALF - 1) / HALF;
+    I.n_half = I.h_e + I.h_f + (I.T.n_w + HALF - 1) / HALF;
+    const int tiles = (I.n_half + 1) / 2;
+    I.k0 = static_cast<int>(static_cast<int64_t>(tiles) * I.split / p.n_splits);
+    I.n = static_cast<int>(static_cast<int64_t>(tiles) * (I.split + 1) / p.n_splits) - I.k0;
+    I.ent0 = rg.base;
+    I.tok0 = rg.base + rg.n_e64;
+    I.win0 = I.tok0 + rg.f + (I.T.w_lo - rg.w0);
+    return true;
+}
+
+// first staged row of a half tile (past the last: finite rows that no query sees)
+__device__ __forceinline__ int64_t half_row(const Item& I, int h) {
+    if (h < I.h_e) return I.ent0 + h * HALF;
+    if (h < I.h_e + I.h_f) return I.tok0 + (h - I.h_e) * HALF;
+    return h < I.n_half ? I.win0 + (h - I.h_e - I.h_f) * HALF : I.win0;
+}
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
 paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
@@ -281,22 +328,6 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
     const uint32_t sbase = smem_u32(smem);
     volatile int* abort_flag = &c.abort_flag;
 
-    Tile T;
-    if (!make_tile(p, blockIdx.x >> 1, PAIR, T) || T.n_new < p.min_chunk) return;   // both CTAs alike
-    const Region rg = region(p, s, T.b, T.ctx, T.n_new);
-    // half tiles of 64 staged rows: entries, first tokens, window
-    const int h_e = (T.n_e + HALF - 1) / HALF, h_f = (T.n_f + HALF - 1) / HALF, h_w = (T.n_w + HALF - 1) / HALF;
-    const int n_half = h_e + h_f + h_w;
-    const int n = (n_half + 1) / 2;
-    const int64_t tok0 = rg.base + rg.n_e64;
-    const int64_t win0 = tok0 + rg.f + (T.w_lo - rg.w0);
-    auto half_row = [&](int h) -> int64_t {
-        if (h < h_e) return rg.base + h * HALF;
-        if (h < h_e + h_f) return tok0 + (h - h_e) * HALF;
-        // (an odd count: the last half repeats finite rows that no query sees)
-        return h < n_half ? win0 + (h - h_e - h_f) * HALF : win0;
-    };
-
     if (tid == 0) {
         for (int i = 0; i < NSLOT; ++i) { mbar_init(smem_u32(&c.full[i]), 1); mbar_init(smem_u32(&c.empty[i]), 1); }
         for (int i = 0; i < 2; ++i) {
@@ -304,9 +335,13 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             mbar_init(smem_u32(&c.s_free[i]), NSOFT);   // the four warps of the tile's group, in both CTAs
             mbar_init(smem_u32(&c.p_full[i]), NSOFT);
             mbar_init(smem_u32(&c.pv_done[i]), 1);
+            mbar_init(smem_u32(&c.item_full[i]), 1);
+            mbar_init(smem_u32(&c.item_free[i]), TAKERS);
         }
-        mbar_init(smem_u32(&c.q_full), 2 * NSOFT);
-        mbar_init(smem_u32(&c.drain), 2);           // both issuing threads
+        mbar_init(smem_u32(&c.q_full), 2 * NQ);
+        mbar_init(smem_u32(&c.q_free), 1);
+        mbar_init(smem_u32(&c.o_free), 2 * NSOFT);
+        mbar_init(smem_u32(&c.drain), 2);               // both issuing threads
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -314,48 +349,93 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(&c.tmem)), "r"(TMEM_COLS) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     }
-
     fence_before();
     __syncthreads();
     cluster_sync();                                 // barriers and TMEM of both CTAs are ready
     fence_after();
     const uint32_t tmem = c.tmem;
+    pdl_wait();                                     // the staged rows are complete, the counter is zero
     bool ok = true;
-    const int rbase = rank * ROWS;                  // first row of this CTA in the tile
-    const int rows = T.rows - rbase < 0 ? 0 : (T.rows - rbase < ROWS ? T.rows - rbase : ROWS);
+    const int rbase = rank * ROWS;                  // first row of this CTA in a tile
+
+    // item k from the mailbox (-1: no more); whole warps
+    const uint32_t item_free_first[2] = {in_first(smem_u32(&c.item_free[0])), in_first(smem_u32(&c.item_free[1]))};
+    auto take_item = [&](int k) -> int {
+        if (!wait_bar(smem_u32(&c.item_full[k & 1]), (k >> 1) & 1, abort_flag)) { ok = false; return -1; }
+        const int it = *reinterpret_cast<volatile int*>(&c.item[k & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(item_free_first[k & 1]);
+        return it;
+    };
 
     if (warp == 8) {
-        // ------------------------------------------------------------ TMA
-        pdl_wait();                                 // the staged rows are complete
+        // ------------------------------------------------------------ TMA, items
         const bool leader = elect_one();
-        auto piece = [&](int pos) -> uint32_t {      // waits for the ring slot, announces both CTAs' bytes
-            const int sl = pos % NSLOT;
-            if (pos >= NSLOT && ok) ok = wait_bar(smem_u32(&c.empty[sl]), ((pos / NSLOT) & 1) ^ 1, abort_flag);
-            if (ok && rank == 0 && leader) mbar_expect(smem_u32(&c.full[sl]), 2 * SLOT);
-            return sbase + R_OFF + sl * SLOT;
+        Item I;
+        auto next_item = [&]() -> int {              // the next item with rows and keys
+            for (;;) {
+                int it = 0;
+                if (lane == 0) it = atomicAdd(s.next, 1);
+                it = __shfl_sync(0xffffffffu, it, 0);
+                if (it >= s.n_items) return -1;
+                Item J;
+                if (!make_item(p, s, it, J)) continue;
+                if (J.n > 0) return it;
+                // no key tile left for this split: its rows' partials weigh nothing
+                for (int r = lane; r < PAIR; r += 32) {
+                    p.part_ml[static_cast<int64_t>(it) * 2 * PAIR + r] = -INFINITY;
+                    p.part_ml[static_cast<int64_t>(it) * 2 * PAIR + PAIR + r] = 0.0f;
+                }
+            }
         };
-        for (int i = 0; i <= n && ok; ++i) {
-            if (i < n) {
-                const int y = static_cast<int>(half_row(2 * i + rank));
-                for (int j = 0; j < 4 && ok; ++j) {
-                    const int pos = k_pos(i) + j;
-                    const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
-                    if (ok && leader) {
-                        tma_2d(dst, &k_map, j * 128, y, bar);
-                        tma_2d(dst + 8192, &k_map, j * 128 + 64, y, bar);
+        auto post = [&](int k, int it) {
+            if (k >= 2 && ok) ok = wait_bar(smem_u32(&c.item_free[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag);
+            if (ok && lane < 2) {
+                uint32_t a, b;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&c.item[k & 1])), "r"(lane));
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(&c.item_full[k & 1])), "r"(lane));
+                asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(a), "r"(it) : "memory");
+                mbar_arrive_cluster(b);
+            }
+            __syncwarp();
+        };
+        int it = -1, base = 0;
+        if (rank == 0) { it = next_item(); post(0, it); } else it = take_item(0);
+        for (int k = 0; it >= 0 && ok; ++k) {
+            int nxt = -1;
+            if (rank == 0) { nxt = next_item(); post(k + 1, nxt); }
+            make_item(p, s, it, I);
+            auto piece = [&](int pos) -> uint32_t {  // waits for the ring slot, announces both CTAs' bytes
+                const int sl = pos % NSLOT;
+                if (pos >= NSLOT && ok) ok = wait_bar(smem_u32(&c.empty[sl]), ((pos / NSLOT) & 1) ^ 1, abort_flag);
+                if (ok && rank == 0 && leader) mbar_expect(smem_u32(&c.full[sl]), 2 * SLOT);
+                return sbase + R_OFF + sl * SLOT;
+            };
+            for (int i = 0; i <= I.n && ok; ++i) {
+                if (i < I.n) {
+                    const int y = static_cast<int>(half_row(I, 2 * (I.k0 + i) + rank));
+                    for (int j = 0; j < 4 && ok; ++j) {
+                        const int pos = base + k_pos(i) + j;
+                        const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
+                        if (ok && leader) {
+                            tma_2d(dst, &k_map, j * 128, y, bar);
+                            tma_2d(dst + 8192, &k_map, j * 128 + 64, y, bar);
+                        }
+                    }
+                }
+                if (i > 0) {
+                    for (int j = 0; j < 4 && ok; ++j) {
+                        const int pos = base + v_pos(i - 1, I.n) + j;
+                        const int y = static_cast<int>(half_row(I, 2 * (I.k0 + i - 1) + (j >> 1))) + (j & 1) * 32;
+                        const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
+                        if (ok && leader)
+#pragma unroll
+                            for (int b = 0; b < 4; ++b) tma_2d(dst + b * 4096, &v_map, rank * 256 + b * 64, y, bar);
                     }
                 }
             }
-            if (i > 0) {
-                for (int j = 0; j < 4 && ok; ++j) {
-                    const int pos = v_pos(i - 1, n) + j;
-                    const int y = static_cast<int>(half_row(2 * (i - 1) + (j >> 1))) + (j & 1) * 32;
-                    const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
-                    if (ok && leader)
-#pragma unroll
-                        for (int b = 0; b < 4; ++b) tma_2d(dst + b * 4096, &v_map, rank * 256 + b * 64, y, bar);
-                }
-            }
+            base += 8 * I.n;
+            it = rank == 0 ? nxt : take_item(k + 1);
         }
         // gave up: copies in flight land within microseconds, before this CTA's memory may go to another
         if (!ok) for (int i = 0; i < 1000; ++i) __nanosleep(1000);
@@ -364,26 +444,37 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_f16(128, 128, 0);
         const uint64_t qd = sdesc(sbase + Q_OFF, 16, 1024);
-        ok = wait_bar(smem_u32(&c.q_full), 0, abort_flag);
-        for (int i = 0; i < n && ok; ++i) {
-            // S(i - 2) has been read
-            if (i >= 2) ok = wait_bar(smem_u32(&c.s_free[i & 1]), ((i - 2) >> 1) & 1, abort_flag);
-            for (int j = 0; j < 4 && ok; ++j) {
-                const int pos = k_pos(i) + j, sl = pos % NSLOT;
-                ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
-                if (!ok) break;
-                fence_after();
-                const uint64_t kd = sdesc(sbase + R_OFF + sl * SLOT, 16, 1024);
-                if (leader) {
+        int base = 0, uses[2] = {0, 0};              // ring position; S buffers used so far
+        Item I;
+        for (int k = 0; ok; ++k) {
+            const int it = take_item(k);
+            if (it < 0) break;
+            make_item(p, s, it, I);
+            ok = wait_bar(smem_u32(&c.q_full), k & 1, abort_flag);
+            for (int i = 0; i < I.n && ok; ++i) {
+                const int b = i & 1, use = (b ? uses[1] : uses[0]) + (i >> 1);
+                if (use > 0) ok = wait_bar(smem_u32(&c.s_free[b]), (use - 1) & 1, abort_flag);     // S's last use has been read
+                for (int j = 0; j < 4 && ok; ++j) {
+                    const int pos = base + k_pos(i) + j, sl = pos % NSLOT;
+                    ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
+                    if (!ok) break;
+                    fence_after();
+                    const uint64_t kd = sdesc(sbase + R_OFF + sl * SLOT, 16, 1024);
+                    if (leader) {
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)   // 16 dims a step: column block kk / 4, 32 bytes a step inside it
-                        mma2(tmem + S_COL + (i & 1) * 64, qd + static_cast<uint32_t>(((2 * j + (kk >> 2)) * 8192 + (kk & 3) * 32) >> 4),
-                             kd + static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id, (j > 0 || kk > 0) ? 1u : 0u);
-                    commit2(smem_u32(&c.empty[sl]));
-                    if (j == 3) commit2(smem_u32(&c.s_full[i & 1]));
+                        for (int kk = 0; kk < 8; ++kk)   // 16 dims a step: column block kk / 4, 32 bytes a step inside it
+                            mma2(tmem + S_COL + b * 64, qd + static_cast<uint32_t>(((2 * j + (kk >> 2)) * 8192 + (kk & 3) * 32) >> 4),
+                                 kd + static_cast<uint32_t>(((kk >> 2) * 8192 + (kk & 3) * 32) >> 4), id, (j > 0 || kk > 0) ? 1u : 0u);
+                        commit2(smem_u32(&c.empty[sl]));
+                        if (j == 3) commit2(smem_u32(&c.s_full[b]));
+                        if (j == 3 && i == I.n - 1) commit2(smem_u32(&c.q_free));
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
+            base += 8 * I.n;
+            uses[0] += (I.n + 1) / 2;
+            uses[1] += I.n / 2;
         }
         if (leader) commit2(smem_u32(&c.drain));
     } else if (warp == 10 && rank == 0) {
@@ -391,98 +482,134 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_f16(128, 256, 1);
         const uint64_t pd = sdesc(sbase + P_OFF, 16, 1024);
-        for (int i = 0; i < n && ok; ++i) {
-            ok = wait_bar(smem_u32(&c.p_full[i & 1]), (i >> 1) & 1, abort_flag);
-            for (int j = 0; j < 4 && ok; ++j) {
-                const int pos = v_pos(i, n) + j, sl = pos % NSLOT;
-                ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
-                if (!ok) break;
-                fence_after();
-                // V: dims are contiguous (MN-major), 64-dim column blocks 4096 B apart, 8 keys 1024 B
-                const uint64_t vd = sdesc(sbase + R_OFF + sl * SLOT, 4096, 1024);
-                if (leader) {
+        int base = 0, uses[2] = {0, 0};
+        Item I;
+        for (int k = 0; ok; ++k) {
+            const int it = take_item(k);
+            if (it < 0) break;
+            make_item(p, s, it, I);
+            if (k > 0) ok = wait_bar(smem_u32(&c.o_free), (k - 1) & 1, abort_flag);               // O of the item before is out
+            for (int i = 0; i < I.n && ok; ++i) {
+                const int b = i & 1, use = (b ? uses[1] : uses[0]) + (i >> 1);
+                ok = wait_bar(smem_u32(&c.p_full[b]), use & 1, abort_flag);
+                for (int j = 0; j < 4 && ok; ++j) {
+                    const int pos = base + v_pos(i, I.n) + j, sl = pos % NSLOT;
+                    ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
+                    if (!ok) break;
+                    fence_after();
+                    // V: dims are contiguous (MN-major), 64-dim column blocks 4096 B apart, 8 keys 1024 B
+                    const uint64_t vd = sdesc(sbase + R_OFF + sl * SLOT, 4096, 1024);
+                    if (leader) {
 #pragma unroll
-                    for (int k2 = 0; k2 < 2; ++k2) {
-                        const int kk = 2 * j + k2;   // 16 keys a step
-                        const uint64_t a = pd + static_cast<uint32_t>(((i & 1) * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
+                        for (int k2 = 0; k2 < 2; ++k2) {
+                            const int kk = 2 * j + k2;   // 16 keys a step
+                            const uint64_t a = pd + static_cast<uint32_t>((b * 16384 + (kk >> 2) * 8192 + (kk & 3) * 32) >> 4);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            mma2(tmem + O_COL + h * 128, a, vd + static_cast<uint32_t>((h * 8192 + k2 * 2048) >> 4), id,
-                                 (i > 0 || kk > 0) ? 1u : 0u);
+                            for (int h = 0; h < 2; ++h)
+                                mma2(tmem + O_COL + h * 128, a, vd + static_cast<uint32_t>((h * 8192 + k2 * 2048) >> 4), id,
+                                     (i > 0 || kk > 0) ? 1u : 0u);
+                        }
+                        commit2(smem_u32(&c.empty[sl]));
+                        if (j == 3) commit2(smem_u32(&c.pv_done[b]));
                     }
-                    commit2(smem_u32(&c.empty[sl]));
-                    if (j == 3) commit2(smem_u32(&c.pv_done[i & 1]));
+                    __syncwarp();
                 }
-                __syncwarp();
             }
+            base += 8 * I.n;
+            uses[0] += (I.n + 1) / 2;
+            uses[1] += I.n / 2;
         }
         if (leader) commit2(smem_u32(&c.drain));
-    } else if (warp < NSOFT) {
-        // ---- this CTA's 64 query rows -> fp16, K-major, 8 rows a warp, every load in flight before the first use;
-        // RMSNorm and RoPE in fp32.  The query is older than the staging kernel (a plain launch): it may be read
-        // before the wait on that kernel.
-        {
-            uint32_t v[8][8];
+    } else if (warp >= 11) {
+        // ------------------------------------------------------------ query rows
+        // 16 rows a warp -> fp16, K-major; RMSNorm and RoPE in fp32.  The first rows are loaded before the buffer is
+        // free (the item before may still be multiplying).
+        constexpr int NB = 8;                        // rows in flight
+        const int w0 = (warp - 11) * (ROWS / NQ);
+        const uint32_t q_first = in_first(smem_u32(&c.q_full));
+        float nw[16];
+        if (p.q_norm_w)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = warp * 8 + k;
-                if (r < rows) {
-                    const uint4* src = reinterpret_cast<const uint4*>(p.q + (T.row0 + rbase + r) * D + lane * 16);
-                    *reinterpret_cast<uint4*>(v[k]) = __ldg(src);
-                    *reinterpret_cast<uint4*>(v[k] + 4) = __ldg(src + 1);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) v[k][i] = 0;
-                }
-            }
+            for (int i = 0; i < 16; ++i) nw[i] = __ldg(p.q_norm_w + lane * 16 + i);
+        Item I;
+        for (int k = 0; ok; ++k) {
+            const int it = take_item(k);
+            if (it < 0) break;
+            make_item(p, s, it, I);
+            const Tile& T = I.T;
+            const int rows = min(max(T.rows - rbase, 0), ROWS);
             int tok = -1;
-            float2 cs = make_float2(1.0f, 0.0f);        // of pair `lane` at the row's position
+            float2 cs = make_float2(1.0f, 0.0f);     // of pair `lane` at the row's position
+#pragma unroll 1
+            for (int r0 = w0; r0 < w0 + ROWS / NQ; r0 += NB) {
+                uint32_t v[NB][8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int r = warp * 8 + k;
-                float f[16];
+                for (int j = 0; j < NB; ++j) {
+                    if (r0 + j < rows) {
+                        const uint4* src = reinterpret_cast<const uint4*>(p.q + (T.row0 + rbase + r0 + j) * D + lane * 16);
+                        *reinterpret_cast<uint4*>(v[j]) = __ldg(src);
+                        *reinterpret_cast<uint4*>(v[j] + 4) = __ldg(src + 1);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[k][i] << 16); f[2 * i + 1] = __uint_as_float(v[k][i] & 0xFFFF0000u); }
-                if (p.q_norm_w) {
-                    float ss = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) ss += f[i] * f[i];
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
-#pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 nw = __ldg(reinterpret_cast<const float4*>(p.q_norm_w + lane * 16 + i));
-                        f[i] *= rr * nw.x; f[i + 1] *= rr * nw.y; f[i + 2] *= rr * nw.z; f[i + 3] *= rr * nw.w;
+                        for (int i = 0; i < 8; ++i) v[j][i] = 0;
                     }
                 }
-                if (p.inv_freq && r < rows) {
-                    const int tk = (T.r0 + rbase + r) / p.H;
-                    if (tk != tok) { tok = tk; cs = rope_cs(p.inv_freq, lane, T.ctx + tk); }
+                if (r0 == w0 && k > 0 && ok) ok = wait_bar(smem_u32(&c.q_free), (k - 1) & 1, abort_flag);
+                float rr[NB];
+                if (p.q_norm_w) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int pair = ((lane * 16 - DN) / 2 + i) & 31;
-                        const float x = __shfl_sync(0xffffffffu, cs.x, pair), y = __shfl_sync(0xffffffffu, cs.y, pair);
-                        if (lane * 16 >= DN) {
-                            const float a = f[2 * i], b = f[2 * i + 1];
-                            f[2 * i] = a * x - b * y;
-                            f[2 * i + 1] = a * y + b * x;
+                    for (int j = 0; j < NB; ++j) {
+                        float ss = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float a = __uint_as_float(v[j][i] << 16), b = __uint_as_float(v[j][i] & 0xFFFF0000u);
+                            ss += a * a + b * b;
+                        }
+                        rr[j] = ss;
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) rr[j] += __shfl_xor_sync(0xffffffffu, rr[j], o);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) rr[j] = rsqrtf(rr[j] / static_cast<float>(D) + p.norm_eps);
+                }
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    const int r = r0 + j;
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[j][i] << 16); f[2 * i + 1] = __uint_as_float(v[j][i] & 0xFFFF0000u); }
+                    if (p.q_norm_w)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = f[i] * rr[j] * nw[i];
+                    if (p.inv_freq && r < rows) {
+                        const int tk = (T.r0 + rbase + r) / p.H;
+                        if (tk != tok) { tok = tk; cs = rope_cs(p.inv_freq, lane, T.ctx + tk); }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int pair = ((lane * 16 - DN) / 2 + i) & 31;
+                            const float x = __shfl_sync(0xffffffffu, cs.x, pair), y = __shfl_sync(0xffffffffu, cs.y, pair);
+                            if (lane * 16 >= DN) {
+                                const float a = f[2 * i], b = f[2 * i + 1];
+                                f[2 * i] = a * x - b * y;
+                                f[2 * i + 1] = a * y + b * x;
+                            }
                         }
                     }
+                    uint8_t* blk = smem + Q_OFF + (lane >> 2) * 8192;
+                    const int ch = (lane & 3) * 2;
+                    *reinterpret_cast<uint4*>(blk + sw128(r, ch)) =
+                        make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                    *reinterpret_cast<uint4*>(blk + sw128(r, ch + 1)) =
+                        make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
                 }
-                uint8_t* blk = smem + Q_OFF + (lane >> 2) * 8192;
-                const int ch = (lane & 3) * 2;
-                *reinterpret_cast<uint4*>(blk + sw128(r, ch)) =
-                    make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-                *reinterpret_cast<uint4*>(blk + sw128(r, ch + 1)) =
-                    make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
             }
             fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.q_full)));
+            if (lane == 0) mbar_arrive_cluster(q_first);
         }
-        pdl_wait();                                  // (the flags of the staged rows)
-
+    } else if (warp < NSOFT) {
         // ------------------------------------------------------------ softmax
         // Group g (4 warps) takes the tiles of parity g, so that a tile's
         // exponentials and its P stores run beside the next tile's; only the
@@ -491,184 +618,220 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const int hk = qd >> 1;                      // which half of the tile's keys
         const int r = (qd & 1) * 32 + lane;          // row of this CTA
         const uint32_t lb = tmem + (static_cast<uint32_t>(qd * 32) << 16);
-        const int rt = min(rbase + r, T.rows - 1);
-        const RowKeys rk = row_keys(p, T, T.ctx + (T.r0 + rt) / p.H);
-        const int w0s = T.n_e + T.n_f;               // first window slot
         const uint32_t p_first = in_first(smem_u32(&c.p_full[g])), s_first = in_first(smem_u32(&c.s_free[g]));
-        float m_l = -INFINITY, l_run = 0.0f;         // this thread's share of l, and the maximum it is relative to
-        uint32_t fl[2];
-        auto flags_of = [&](int i) {
-            const uint8_t* f = s.flags + (i < n ? half_row(2 * i + hk) : rg.base) + lane;
-            fl[0] = f[0];
-            fl[1] = f[32];
-        };
-        flags_of(g);
-        for (int i = g; i < n; i += 2) {
-            const int h = 2 * i + hk;
-            // keys that this row sees among the half tile's 64, as bits
-            auto below = [](int k) -> unsigned { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
-            unsigned vis[2], bad = 0;
+        const uint32_t o_first = in_first(smem_u32(&c.o_free));
+        int uses[2] = {0, 0};                        // of each parity's buffers, so far
+        Item I;
+        for (int kk = 0;; ++kk) {
+            // one warp takes the item for all eight (they meet at barriers: all go on, or none)
+            if (warp == 0) {
+                const int it = take_item(kk);
+                if (lane == 0) c.soft_item = it;
+            }
+            bar_sync(5, NSOFT * 32);
+            const int it = c.soft_item;
+            if (it < 0) break;
+            make_item(p, s, it, I);
+            const Tile& T = I.T;
+            const int n = I.n;
+            const int rows = min(max(T.rows - rbase, 0), ROWS);
+            const int rt = min(rbase + r, T.rows - 1);
+            const int tok = (T.r0 + rt) / p.H;
+            const RowKeys rk = row_keys(p, T, T.ctx + tok);
+            const int w0s = T.n_e + T.n_f;           // first window slot
+            float m_l = -INFINITY, l_run = 0.0f;     // this thread's share of l, and the maximum it is relative to
+            uint32_t fl[2];
+            auto flags_of = [&](int i) {
+                const uint8_t* f = s.flags + (i < n ? half_row(I, 2 * (I.k0 + i) + hk) : I.ent0) + lane;
+                fl[0] = f[0];
+                fl[1] = f[32];
+            };
+            flags_of(g);
+            for (int i = g; i < n; i += 2) {
+                const int h = 2 * (I.k0 + i) + hk, use = uses[g] + (i >> 1);
+                // keys that this row sees among the half tile's 64, as bits
+                auto below = [](int k) -> unsigned { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
+                unsigned vis[2], bad = 0;
 #pragma unroll
-            for (int z = 0; z < 2; ++z) {
-                const unsigned gone = __ballot_sync(0xffffffffu, fl[z] & 1u), nf = __ballot_sync(0xffffffffu, fl[z] & 2u);
-                if (h < h_e) {
-                    vis[z] = below(rk.e_lim - (h * HALF + z * 32));
-                } else if (h < h_e + h_f) {
-                    vis[z] = below(T.n_f - ((h - h_e) * HALF + z * 32));
-                } else {
-                    const int k0 = w0s + (h - h_e - h_f) * HALF + z * 32;     // slot of the first of these keys
-                    vis[z] = h < n_half ? below(rk.w_hi + 1 - k0) & (~below(rk.w_from - k0) | below(rk.f_to - k0)) : 0u;
+                for (int z = 0; z < 2; ++z) {
+                    const unsigned gone = __ballot_sync(0xffffffffu, fl[z] & 1u), nf = __ballot_sync(0xffffffffu, fl[z] & 2u);
+                    if (h < I.h_e) {
+                        vis[z] = below(rk.e_lim - (h * HALF + z * 32));
+                    } else if (h < I.h_e + I.h_f) {
+                        vis[z] = below(T.n_f - ((h - I.h_e) * HALF + z * 32));
+                    } else {
+                        const int k0 = w0s + (h - I.h_e - I.h_f) * HALF + z * 32;     // slot of the first of these keys
+                        vis[z] = h < I.n_half ? below(rk.w_hi + 1 - k0) & (~below(rk.w_from - k0) | below(rk.f_to - k0)) : 0u;
+                    }
+                    vis[z] &= ~gone;
+                    bad |= vis[z] & nf;
                 }
-                vis[z] &= ~gone;
-                bad |= vis[z] & nf;
-            }
-            flags_of(i + 2);
-            if (ok) ok = wait_bar(smem_u32(&c.s_full[g]), (i >> 1) & 1, abort_flag);
-            fence_after();
-            float v[64];
-            {
-                uint32_t sr[32];
-                tmem_ld32(lb + S_COL + g * 64, sr);
-                uint32_t s2[32];
-                tmem_ld32(lb + S_COL + g * 64 + 32, s2);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) { v[j] = __uint_as_float(sr[j]); v[32 + j] = __uint_as_float(s2[j]); }
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(s_first);            // S may be overwritten
-            if (!__all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu))
-#pragma unroll
-                for (int j = 0; j < 64; ++j) v[j] = ((vis[j >> 5] >> (j & 31)) & 1u) ? v[j] : -INFINITY;
-            float t[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) t[j] = fmaxf(fmaxf(v[j], v[j + 16]), fmaxf(v[j + 32], v[j + 48]));
-#pragma unroll
-            for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-                for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
-            c.mx[g][hk][r] = t[0];
-            bar_sync(1 + g, 128);
-            // the scale is positive: the largest raw logit scaled is the largest logit
-            const float m_tile = fmaxf(t[0], c.mx[g][hk ^ 1][r]) * p.scale_log2;
-            // the maximum after tile i - 1, from the other group
-            // (a barrier of this group either way, before c.mx is written again)
-            if (i > 0) bar_sync(3 + (i & 1), 256); else bar_sync(1 + g, 128);
-            const float m_old = i > 0 ? c.m[(i - 1) & 1][r] : -INFINITY;
-            bool resc = false;
-            float m_new = m_old;
-            if (m_old == -INFINITY) {
-                m_new = m_tile;                      // nothing seen before: O and l are zero
-            } else if (m_tile > m_old + GROW) {
-                resc = true;
-                m_new = m_tile;
-            }
-            if (hk == 0) c.m[i & 1][r] = m_new;
-            if (i + 1 < n) asm volatile("bar.arrive %0, 256;" :: "r"(3 + ((i + 1) & 1)) : "memory");
-            const float ref = m_new == -INFINITY ? 0.0f : m_new;
-            uint32_t pk[32];
-            float ps[16];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                pk[j] = pack_half2(ex2(fmaf(v[2 * j], p.scale_log2, -ref)), ex2(fmaf(v[2 * j + 1], p.scale_log2, -ref)));
-                const float2 f = unpack_half2(pk[j]);    // l sums the probabilities as PV uses them
-                if (j < 16) ps[j] = f.x + f.y; else ps[j - 16] += f.x + f.y;
-            }
-#pragma unroll
-            for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-                for (int j = 0; j < w; ++j) ps[j] += ps[j + w];
-            l_run = (m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_new)) + ps[0];
-            m_l = m_new;
-            if (bad) l_run = __int_as_float(0x7fc00000);             // a visible key that is not finite
-            if (i >= 2 && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), ((i - 2) >> 1) & 1, abort_flag);   // P's buffer is free
-            if (__any_sync(0xffffffffu, resc)) {
-                // O must hold still: PV(i - 1) complete (PV(i - 3), the barrier's phase before, completed ahead of
-                // PV(i - 2), which has been waited for; PV(i) waits for this P)
-                if (ok) ok = wait_bar(smem_u32(&c.pv_done[g ^ 1]), ((i - 1) >> 1) & 1, abort_flag);
+                flags_of(i + 2);
+                if (ok) ok = wait_bar(smem_u32(&c.s_full[g]), use & 1, abort_flag);
                 fence_after();
-                const float alpha = resc ? ex2(m_old - m_new) : 1.0f;
-#pragma unroll 1
-                for (int q = 0; q < 8; ++q) {
-                    uint32_t o[32];
-                    const uint32_t a = lb + O_COL + q * 32;
-                    tmem_ld32(a, o);
+                float v[64];
+                {
+                    uint32_t sr[32];
+                    tmem_ld32(lb + S_COL + g * 64, sr);
+                    uint32_t s2[32];
+                    tmem_ld32(lb + S_COL + g * 64 + 32, s2);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                    tmem_st32(a, o);
+                    for (int j = 0; j < 32; ++j) { v[j] = __uint_as_float(sr[j]); v[32 + j] = __uint_as_float(s2[j]); }
                 }
-                tmem_wait_st();
-            }
-            uint8_t* pb = smem + P_OFF + g * 16384 + hk * 8192;
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(s_first);            // S may be overwritten
+                if (!__all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu))
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                *reinterpret_cast<uint4*>(pb + sw128(r, j)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
-            fence_async();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(p_first);
-        }
-        // the last tile's group waits for the last PV (it has seen the phase before; the other group may not have)
-        if (g == ((n - 1) & 1) && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), ((n - 1) >> 1) & 1, abort_flag);
-        bar_sync(5, NSOFT * 32);
-        fence_after();
-        const float m_used = c.m[(n - 1) & 1][r];
-        c.l[hk * 2 + g][r] = m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_used);
-        const int sub = g;                           // the half of the row's dims that this thread writes out
-        // P's memory is free again: the RoPE table for the way back
-        const int tok_first = (T.r0 + rbase) / p.H;  // token (inside the request) of this CTA's row 0
-        const int tok_last = rows > 0 ? (T.r0 + rbase + rows - 1) / p.H : tok_first - 1;
-        float2* s_cs = reinterpret_cast<float2*>(smem + P_OFF);     // [token][32]
-        if (p.inv_freq)
-            for (int w = tid; w < (tok_last - tok_first + 1) * (DR / 2); w += NSOFT * 32)
-                s_cs[w] = rope_cs(p.inv_freq, w % (DR / 2), T.ctx + tok_first + w / (DR / 2));
-        bar_sync(5, NSOFT * 32);
-        float l = c.l[0][r] + c.l[1][r] + c.l[2][r] + c.l[3][r];
-        if (p.sink && (m_used != -INFINITY || l != l)) l += ex2(__ldg(p.sink + (T.r0 + rt) % p.H) * LOG2E - m_used);
-        float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        if (*abort_flag) inv = __int_as_float(0x7fc00000);
-        // O: row r, dims 256 hk + 128 sub .. + 127, as bf16 into the ring's memory (free: every piece was consumed),
-        // 16-byte chunks swizzled by row, then whole rows out
-        uint8_t* ob = smem + R_OFF;
+                    for (int j = 0; j < 64; ++j) v[j] = ((vis[j >> 5] >> (j & 31)) & 1u) ? v[j] : -INFINITY;
+                float t[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) t[j] = fmaxf(fmaxf(v[j], v[j + 16]), fmaxf(v[j + 32], v[j + 48]));
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                    for (int j = 0; j < w; ++j) t[j] = fmaxf(t[j], t[j + w]);
+                c.mx[g][hk][r] = t[0];
+                bar_sync(1 + g, 128);
+                // the scale is positive: the largest raw logit scaled is the largest logit
+                const float m_tile = fmaxf(t[0], c.mx[g][hk ^ 1][r]) * p.scale_log2;
+                // the maximum after tile i - 1, from the other group
+                // (a barrier of this group either way, before c.mx is written again)
+                if (i > 0) bar_sync(3 + (i & 1), 256); else bar_sync(1 + g, 128);
+                const float m_old = i > 0 ? c.m[(i - 1) & 1][r] : -INFINITY;
+                bool resc = false;
+                float m_new = m_old;
+                if (m_old == -INFINITY) {
+                    m_new = m_tile;                  // nothing seen before: O and l are zero
+                } else if (m_tile > m_old + GROW) {
+                    resc = true;
+                    m_new = m_tile;
+                }
+                if (hk == 0) c.m[i & 1][r] = m_new;
+                if (i + 1 < n) asm volatile("bar.arrive %0, 256;" :: "r"(3 + ((i + 1) & 1)) : "memory");
+                const float ref = m_new == -INFINITY ? 0.0f : m_new;
+                uint32_t pk[32];
+                float ps[16];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    pk[j] = pack_half2(ex2(fmaf(v[2 * j], p.scale_log2, -ref)), ex2(fmaf(v[2 * j + 1], p.scale_log2, -ref)));
+                    const float2 f = unpack_half2(pk[j]);    // l sums the probabilities as PV uses them
+                    if (j < 16) ps[j] = f.x + f.y; else ps[j - 16] += f.x + f.y;
+                }
+#pragma unroll
+                for (int w = 8; w >= 1; w >>= 1)
+#pragma unroll
+                    for (int j = 0; j < w; ++j) ps[j] += ps[j + w];
+                l_run = (m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_new)) + ps[0];
+                m_l = m_new;
+                if (bad) l_run = __int_as_float(0x7fc00000);             // a visible key that is not finite
+                if (use > 0 && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (use - 1) & 1, abort_flag);   // P's buffer is free
+                if (__any_sync(0xffffffffu, resc)) {
+                    // O must hold still: PV(i - 1) complete (the barrier's phase before belongs to a PV that completed
+                    // ahead of the one just waited for; PV(i) waits for this P)
+                    if (ok) ok = wait_bar(smem_u32(&c.pv_done[g ^ 1]), (uses[g ^ 1] + ((i - 1) >> 1)) & 1, abort_flag);
+                    fence_after();
+                    const float alpha = resc ? ex2(m_old - m_new) : 1.0f;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-            uint32_t o[32];
-            tmem_ld32(lb + O_COL + sub * 128 + q * 32, o);
-            tmem_wait_ld();
-            float f[32];
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[32];
+                        const uint32_t a = lb + O_COL + q * 32;
+                        tmem_ld32(a, o);
+                        tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
-            const int d0 = hk * 256 + sub * 128 + q * 32;
-            if (p.inv_freq && d0 >= DN) {
-                const float2* cs = s_cs + ((T.r0 + rt) / p.H - tok_first) * (DR / 2) + (d0 - DN) / 2;
-                if (r < rows)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const float x = f[2 * j], y = f[2 * j + 1];
-                        f[2 * j] = x * cs[j].x + y * cs[j].y;
-                        f[2 * j + 1] = y * cs[j].x - x * cs[j].y;
+                        for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        tmem_st32(a, o);
                     }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t w[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[8 * j + 2 * k], f[8 * j + 2 * k + 1]);
-                    w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+                    tmem_wait_st();
                 }
-                *reinterpret_cast<uint4*>(ob + r * 1024 + (((d0 / 8 + j) ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-        }
-        bar_sync(5, NSOFT * 32);
-        for (int rr = warp; rr < rows; rr += NSOFT) {
-            uint16_t* dst = p.out + (T.row0 + rbase + rr) * D;
+                uint8_t* pb = smem + P_OFF + g * 16384 + hk * 8192;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int ch = k * 32 + lane;
-                *reinterpret_cast<uint4*>(dst + ch * 8) = *reinterpret_cast<const uint4*>(ob + rr * 1024 + ((ch ^ (rr & 7)) << 4));
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(pb + sw128(r, j)) = make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+                fence_async();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(p_first);
+            }
+            // ---- the item's output.  The last tile's group waits for the last PV (it has seen the phase before; the
+            // other group may not have)
+            if (g == ((n - 1) & 1) && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (uses[g] + ((n - 1) >> 1)) & 1, abort_flag);
+            uses[0] += (n + 1) / 2;
+            uses[1] += n / 2;
+            bar_sync(5, NSOFT * 32);
+            fence_after();
+            const float m_used = c.m[(n - 1) & 1][r];
+            c.l[hk * 2 + g][r] = m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_used);
+            bar_sync(5, NSOFT * 32);
+            float l = c.l[0][r] + c.l[1][r] + c.l[2][r] + c.l[3][r];
+            const bool parts = p.n_splits > 1;
+            if (parts && hk == 0 && g == 0) {
+                float* ml = p.part_ml + static_cast<int64_t>(it) * 2 * PAIR + rbase + r;
+                ml[0] = m_used;
+                ml[PAIR] = *abort_flag ? __int_as_float(0x7fc00000) : l;
+            }
+            if (!parts && p.sink && (m_used != -INFINITY || l != l)) l += ex2(__ldg(p.sink + (T.r0 + rt) % p.H) * LOG2E - m_used);
+            float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if (*abort_flag) inv = __int_as_float(0x7fc00000);
+            // RoPE back: pair `lane` at this row's position, when the warp's rows are one token's
+            const bool rot = !parts && p.inv_freq && hk == 1 && g == 1;      // this warp holds the RoPE dims
+            const bool one_tok = __all_sync(0xffffffffu, tok == __shfl_sync(0xffffffffu, tok, 0));
+            float2 cs = make_float2(1.0f, 0.0f);
+            if (rot && one_tok) cs = rope_cs(p.inv_freq, lane, T.ctx + tok);
+            // O: row r, dims 256 hk + 128 g .. + 127, half of them at a time through the P buffers (free now): 64 rows of
+            // four 128-byte segments, one per (hk, g), 16-byte chunks swizzled by row; then whole segments out
+            uint8_t* ob = smem + P_OFF;
+#pragma unroll 1
+            for (int q2 = 0; q2 < 2; ++q2) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(lb + O_COL + g * 128 + q2 * 64 + q * 32, o);
+                    tmem_wait_ld();
+                    if (q2 == 1 && q == 1) {             // O has been read
+                        fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(o_first);
+                    }
+                    float f[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
+                    if (rot && q2 == 1) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float2 z;
+                            if (one_tok) {
+                                z.x = __shfl_sync(0xffffffffu, cs.x, q * 16 + j);
+                                z.y = __shfl_sync(0xffffffffu, cs.y, q * 16 + j);
+                            } else {
+                                z = rope_cs(p.inv_freq, q * 16 + j, T.ctx + tok);
+                            }
+                            const float x = f[2 * j], y = f[2 * j + 1];
+                            f[2 * j] = x * z.x + y * z.y;
+                            f[2 * j + 1] = y * z.x - x * z.y;
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float x = f[8 * j + 2 * k], y = f[8 * j + 2 * k + 1];
+                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+                            w[k] = parts ? pack_half2(x, y) : *reinterpret_cast<const uint32_t*>(&b2);
+                        }
+                        const int ch = (hk * 2 + g) * 8 + q * 4 + j;
+                        *reinterpret_cast<uint4*>(ob + r * 512 + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                bar_sync(5, NSOFT * 32);
+                uint16_t* dst = parts ? p.part_o + (static_cast<int64_t>(it) * PAIR + rbase) * D : p.out + (T.row0 + rbase) * D;
+                // lane = (segment, chunk): dims 128 segment + 64 q2 + 8 chunk
+                for (int rr = warp; rr < rows; rr += NSOFT)
+                    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(rr) * D + (lane >> 3) * 128 + q2 * 64 + (lane & 7) * 8) =
+                        *reinterpret_cast<const uint4*>(ob + rr * 512 + ((lane ^ (rr & 7)) << 4));
+                bar_sync(5, NSOFT * 32);
             }
         }
         fence_before();
@@ -715,29 +878,31 @@ static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box
 
 }  // namespace tcp
 
-// Workspace of the chunk kernels: staged rows (fp16), then a flag byte a row.
+// Workspace: staged rows (fp16), a flag byte a row, the item counter.
 static int64_t stage_per_req(int64_t max_entries, int W, int n_first) {
     return ((max_entries + 63) & ~int64_t(63)) + n_first + W + 63;
 }
 int64_t tc_stage_rows(int64_t n_rows, int B, int64_t max_entries, int W, int n_first) {
     return B * stage_per_req(max_entries, W, n_first) + n_rows;
 }
-size_t tc_stage_bytes(int64_t rows) { return (static_cast<size_t>(rows) * (tcp::D * 2 + 1) + 255) & ~size_t(255); }
+size_t tc_stage_bytes(int64_t rows) { return (static_cast<size_t>(rows) * (tcp::D * 2 + 1) + 16 + 255) & ~size_t(255); }
 
-int tc_chunk_launch(const Params& p, int64_t max_entries, void* ws, cudaStream_t st) {
+int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* ws, cudaStream_t st) {
     tcp::Stage s;
     s.per_req = stage_per_req(max_entries, p.W, p.n_first);
     s.bound = tc_stage_rows(p.n_rows, p.B, max_entries, p.W, p.n_first);
     s.rows = static_cast<uint16_t*>(ws);
     s.flags = reinterpret_cast<uint8_t*>(s.rows + s.bound * tcp::D);
+    s.next = reinterpret_cast<int*>(s.flags + ((s.bound + 15) & ~int64_t(15)));
+    s.n_items = static_cast<int>(tiles * p.n_splits);
     CUtensorMap km, vm;
     if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF) || !tcp::make_map(&vm, s.rows, s.bound, 32)) return HCA_ERR_CUDA;
     cudaError_t e = cudaFuncSetAttribute(tcp::paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcp::SMEM);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound, 8)), 256, 0, st>>>(p, s);
     HCA_CHECK_LAUNCH();
-    const int64_t tiles = p.n_rows * p.H / tcp::PAIR + p.B;
-    e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * tiles)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm);
+    const int64_t pairs = sm_count() / 2 < s.n_items ? sm_count() / 2 : s.n_items;
+    e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     HCA_CHECK_LAUNCH();
     return HCA_OK;
