@@ -272,13 +272,22 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 8 * i - 4; }
 __device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 8 * i + 4 : 8 * i + 8; }
 
+// One item: a tile's rows and the key tiles [k0, k0 + n) of its split.
+struct Item {
+    Tile T;
+    int index;                  // tile x splits + split; -1: no more items
+    int k0, n;
+    int h_e, h_f, n_half;       // half tiles of 64 staged rows: entries, first tokens, all
+    int64_t ent0, tok0, win0;   // staged rows of the first entry, first token, first window token
+};
+
 struct Ctrl {
     uint64_t full[NSLOT], empty[NSLOT], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free;
     uint64_t item_full[2], item_free[2], drain;
-    float mx[2][2][ROWS];       // [group][key half][row]: a tile's largest raw logit
+    Item item[2];
+    float mx[2][2][ROWS];       // [group][key half][row]: a tile's largest raw logit; at the end each thread's l
     float m[2][ROWS];           // [tile parity]: the running maximum (base 2) after the tile
-    float l[4][ROWS];
-    int item[2], soft_item;
+    Item soft_item;             // the softmax warps' copy
     uint32_t tmem;
     int abort_flag;
 };
@@ -287,25 +296,17 @@ static_assert(CTRL_OFF + sizeof(Ctrl) <= SMEM, "shared memory");
 // softmax, TMA and the query warps of the second
 constexpr int TAKERS = 3 + NQ + 2 + NQ;
 
-// One item: a tile's rows and the key tiles [k0, k0 + n) of its split.
-struct Item {
-    Tile T;
-    int split, k0, n;
-    int h_e, h_f, n_half;       // half tiles of 64 staged rows: entries, first tokens, all
-    int64_t ent0, tok0, win0;   // staged rows of the first entry, first token, first window token
-};
-
 __device__ __forceinline__ bool make_item(const Params& p, const Stage& s, int item, Item& I) {
-    const int t = item / p.n_splits;
-    I.split = item - t * p.n_splits;
+    const int t = item / p.n_splits, split = item - t * p.n_splits;
+    I.index = item;
     if (!make_tile(p, t, PAIR, I.T)) return false;
     const Region rg = region(p, s, I.T.b, I.T.ctx, I.T.n_new);
     I.h_e = (I.T.n_e + HALF - 1) / HALF;
     I.h_f = (I.T.n_f + HALF - 1) / HALF;
     I.n_half = I.h_e + I.h_f + (I.T.n_w + HALF - 1) / HALF;
     const int tiles = (I.n_half + 1) / 2;
-    I.k0 = static_cast<int>(static_cast<int64_t>(tiles) * I.split / p.n_splits);
-    I.n = static_cast<int>(static_cast<int64_t>(tiles) * (I.split + 1) / p.n_splits) - I.k0;
+    I.k0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.n_splits);
+    I.n = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.n_splits) - I.k0;
     I.ent0 = rg.base;
     I.tok0 = rg.base + rg.n_e64;
     I.win0 = I.tok0 + rg.f + (I.T.w_lo - rg.w0);
@@ -317,6 +318,26 @@ __device__ __forceinline__ int64_t half_row(const Item& I, int h) {
     if (h < I.h_e) return I.ent0 + h * HALF;
     if (h < I.h_e + I.h_f) return I.tok0 + (h - I.h_e) * HALF;
     return h < I.n_half ? I.win0 + (h - I.h_e - I.h_f) * HALF : I.win0;
+}
+
+// RoPE back of 32 dims (pairs pair0 ..) of a row whose neighbours in the warp are
+// other tokens' (few heads): rolled and out of line, to keep the usual path short.
+__device__ __noinline__ void rope_back_16(float* g, const float* inv_freq, int pair0, int64_t pos) {
+#pragma unroll 1
+    for (int j = 0; j < 16; ++j) {
+        const float2 z = rope_cs(inv_freq, pair0 + j, pos);
+        const float x = g[2 * j], y = g[2 * j + 1];
+        g[2 * j] = x * z.x + y * z.y;
+        g[2 * j + 1] = y * z.x - x * z.y;
+    }
+}
+__device__ __forceinline__ void rope_back_rows(float (&f)[32], const float* inv_freq, int pair0, int64_t pos) {
+    float g[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) g[j] = f[j];
+    rope_back_16(g, inv_freq, pair0, pos);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) f[j] = g[j];
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
@@ -358,53 +379,61 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
     bool ok = true;
     const int rbase = rank * ROWS;                  // first row of this CTA in a tile
 
-    // item k from the mailbox (-1: no more); whole warps
-    const uint32_t item_free_first[2] = {in_first(smem_u32(&c.item_free[0])), in_first(smem_u32(&c.item_free[1]))};
-    auto take_item = [&](int k) -> int {
-        if (!wait_bar(smem_u32(&c.item_full[k & 1]), (k >> 1) & 1, abort_flag)) { ok = false; return -1; }
-        const int it = *reinterpret_cast<volatile int*>(&c.item[k & 1]);
+    // item k from the mailbox (false: no more); whole warps
+    auto take_item = [&](int k, Item& I) -> bool {
+        if (!wait_bar(smem_u32(&c.item_full[k & 1]), (k >> 1) & 1, abort_flag)) { ok = false; I.index = -1; return false; }
+        I = c.item[k & 1];
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(item_free_first[k & 1]);
-        return it;
+        if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.item_free[k & 1])));
+        return I.index >= 0;
     };
 
     if (warp == 8) {
         // ------------------------------------------------------------ TMA, items
         const bool leader = elect_one();
-        Item I;
-        auto next_item = [&]() -> int {              // the next item with rows and keys
+        // the next item with rows and keys, posted to both CTAs: where and how much is worked out once, here
+        auto post_next = [&](int k, Item& J) {
             for (;;) {
                 int it = 0;
                 if (lane == 0) it = atomicAdd(s.next, 1);
                 it = __shfl_sync(0xffffffffu, it, 0);
-                if (it >= s.n_items) return -1;
-                Item J;
+                J.index = -1;
+                if (it >= s.n_items) break;
                 if (!make_item(p, s, it, J)) continue;
-                if (J.n > 0) return it;
+                if (J.n > 0) break;
                 // no key tile left for this split: its rows' partials weigh nothing
                 for (int r = lane; r < PAIR; r += 32) {
                     p.part_ml[static_cast<int64_t>(it) * 2 * PAIR + r] = -INFINITY;
                     p.part_ml[static_cast<int64_t>(it) * 2 * PAIR + PAIR + r] = 0.0f;
                 }
             }
-        };
-        auto post = [&](int k, int it) {
             if (k >= 2 && ok) ok = wait_bar(smem_u32(&c.item_free[k & 1]), ((k >> 1) & 1) ^ 1, abort_flag);
-            if (ok && lane < 2) {
-                uint32_t a, b;
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(&c.item[k & 1])), "r"(lane));
-                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(b) : "r"(smem_u32(&c.item_full[k & 1])), "r"(lane));
-                asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(a), "r"(it) : "memory");
-                mbar_arrive_cluster(b);
+            if (!ok) return;
+            if (lane == 0) c.item[k & 1] = J;
+            __syncwarp();
+            // lane w: word w into the second CTA
+            constexpr int WORDS = sizeof(Item) / 4;
+            static_assert(WORDS <= 32 && sizeof(Item) % 4 == 0, "one word a lane");
+            if (lane < WORDS) {
+                const uint32_t at = smem_u32(&c.item[k & 1]) + lane * 4;
+                uint32_t far, w;
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(at) : "memory");
+                asm volatile("mapa.shared::cluster.u32 %0, %1, 1;" : "=r"(far) : "r"(at));
+                asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(far), "r"(w) : "memory");
+                asm volatile("fence.acq_rel.cluster;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane < 2) {
+                uint32_t bar;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&c.item_full[k & 1])), "r"(lane));
+                mbar_arrive_cluster(bar);
             }
             __syncwarp();
         };
-        int it = -1, base = 0;
-        if (rank == 0) { it = next_item(); post(0, it); } else it = take_item(0);
-        for (int k = 0; it >= 0 && ok; ++k) {
-            int nxt = -1;
-            if (rank == 0) { nxt = next_item(); post(k + 1, nxt); }
-            make_item(p, s, it, I);
+        Item I, J;
+        int base = 0;
+        if (rank == 0) post_next(0, I); else take_item(0, I);
+        for (int k = 0; I.index >= 0 && ok; ++k) {
             auto piece = [&](int pos) -> uint32_t {  // waits for the ring slot, announces both CTAs' bytes
                 const int sl = pos % NSLOT;
                 if (pos >= NSLOT && ok) ok = wait_bar(smem_u32(&c.empty[sl]), ((pos / NSLOT) & 1) ^ 1, abort_flag);
@@ -423,6 +452,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                         }
                     }
                 }
+                if (i == 0 && rank == 0 && ok) post_next(k + 1, J);      // behind the item's first keys
                 if (i > 0) {
                     for (int j = 0; j < 4 && ok; ++j) {
                         const int pos = base + v_pos(i - 1, I.n) + j;
@@ -435,7 +465,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 }
             }
             base += 8 * I.n;
-            it = rank == 0 ? nxt : take_item(k + 1);
+            if (rank == 0) I = J; else take_item(k + 1, I);
         }
         // gave up: copies in flight land within microseconds, before this CTA's memory may go to another
         if (!ok) for (int i = 0; i < 1000; ++i) __nanosleep(1000);
@@ -447,9 +477,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         int base = 0, uses[2] = {0, 0};              // ring position; S buffers used so far
         Item I;
         for (int k = 0; ok; ++k) {
-            const int it = take_item(k);
-            if (it < 0) break;
-            make_item(p, s, it, I);
+            if (!take_item(k, I)) break;
             ok = wait_bar(smem_u32(&c.q_full), k & 1, abort_flag);
             for (int i = 0; i < I.n && ok; ++i) {
                 const int b = i & 1, use = (b ? uses[1] : uses[0]) + (i >> 1);
@@ -485,9 +513,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         int base = 0, uses[2] = {0, 0};
         Item I;
         for (int k = 0; ok; ++k) {
-            const int it = take_item(k);
-            if (it < 0) break;
-            make_item(p, s, it, I);
+            if (!take_item(k, I)) break;
             if (k > 0) ok = wait_bar(smem_u32(&c.o_free), (k - 1) & 1, abort_flag);               // O of the item before is out
             for (int i = 0; i < I.n && ok; ++i) {
                 const int b = i & 1, use = (b ? uses[1] : uses[0]) + (i >> 1);
@@ -522,88 +548,85 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         if (leader) commit2(smem_u32(&c.drain));
     } else if (warp >= 11) {
         // ------------------------------------------------------------ query rows
-        // 16 rows a warp -> fp16, K-major; RMSNorm and RoPE in fp32.  The first rows are loaded before the buffer is
-        // free (the item before may still be multiplying).
-        constexpr int NB = 8;                        // rows in flight
+        // 16 rows a warp, copied as stored (bf16) to where the fp16 values go, then converted in place, each lane what
+        // it copied itself; RMSNorm and RoPE in fp32.  Rolled loops: an unrolled form of this (8 rows in registers)
+        // took 14K clocks an item, most of them waiting for instructions.
         const int w0 = (warp - 11) * (ROWS / NQ);
+        uint8_t* const my = smem + Q_OFF + (lane >> 2) * 8192;       // dims 16 lane .. + 15: two chunks of column block lane / 4
+        const int ch = (lane & 3) * 2;
         const uint32_t q_first = in_first(smem_u32(&c.q_full));
-        float nw[16];
-        if (p.q_norm_w)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) nw[i] = __ldg(p.q_norm_w + lane * 16 + i);
         Item I;
         for (int k = 0; ok; ++k) {
-            const int it = take_item(k);
-            if (it < 0) break;
-            make_item(p, s, it, I);
+            if (!take_item(k, I)) break;
             const Tile& T = I.T;
             const int rows = min(max(T.rows - rbase, 0), ROWS);
-            int tok = -1;
-            float2 cs = make_float2(1.0f, 0.0f);     // of pair `lane` at the row's position
+            const uint16_t* src = p.q + (T.row0 + rbase + w0) * D + lane * 16;
+            // the rows on their way to L2 while the item before still uses the buffer
+            if (k > 0) {
+                if (lane < 8)
 #pragma unroll 1
-            for (int r0 = w0; r0 < w0 + ROWS / NQ; r0 += NB) {
-                uint32_t v[NB][8];
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    if (r0 + j < rows) {
-                        const uint4* src = reinterpret_cast<const uint4*>(p.q + (T.row0 + rbase + r0 + j) * D + lane * 16);
-                        *reinterpret_cast<uint4*>(v[j]) = __ldg(src);
-                        *reinterpret_cast<uint4*>(v[j] + 4) = __ldg(src + 1);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[j][i] = 0;
-                    }
+                    for (int r = 0; r < ROWS / NQ; ++r)
+                        if (w0 + r < rows) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + static_cast<int64_t>(r) * D + lane * 48));
+                ok = wait_bar(smem_u32(&c.q_free), (k - 1) & 1, abort_flag);
+            }
+#pragma unroll 4
+            for (int r = 0; r < ROWS / NQ; ++r) {
+                const uint32_t d0 = smem_u32(my + sw128(w0 + r, ch)), d1 = smem_u32(my + sw128(w0 + r, ch + 1));
+                if (w0 + r < rows) {
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(d0), "l"(src + static_cast<int64_t>(r) * D) : "memory");
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(d1), "l"(src + static_cast<int64_t>(r) * D + 8) : "memory");
+                } else {
+                    *reinterpret_cast<uint4*>(my + sw128(w0 + r, ch)) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4*>(my + sw128(w0 + r, ch + 1)) = make_uint4(0, 0, 0, 0);
                 }
-                if (r0 == w0 && k > 0 && ok) ok = wait_bar(smem_u32(&c.q_free), (k - 1) & 1, abort_flag);
-                float rr[NB];
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            int tok = -1;
+            float2 cs[8];                            // of this lane's pairs (lanes that hold RoPE dims), at the row's position
+#pragma unroll 1
+            for (int r = 0; r < ROWS / NQ && w0 + r < rows; ++r) {
+                uint4* c0 = reinterpret_cast<uint4*>(my + sw128(w0 + r, ch));
+                uint4* c1 = reinterpret_cast<uint4*>(my + sw128(w0 + r, ch + 1));
+                const uint4 a0 = *c0, a1 = *c1;
+                const uint32_t v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                float f[16];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[i] << 16); f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u); }
                 if (p.q_norm_w) {
+                    float ss = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        float ss = 0.0f;
+                    for (int i = 0; i < 16; ++i) ss += f[i] * f[i];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float a = __uint_as_float(v[j][i] << 16), b = __uint_as_float(v[j][i] & 0xFFFF0000u);
-                            ss += a * a + b * b;
-                        }
-                        rr[j] = ss;
+                    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
+#pragma unroll
+                    for (int i = 0; i < 16; i += 4) {
+                        const float4 nw = __ldg(reinterpret_cast<const float4*>(p.q_norm_w + lane * 16 + i));
+                        f[i] *= rr * nw.x; f[i + 1] *= rr * nw.y; f[i + 2] *= rr * nw.z; f[i + 3] *= rr * nw.w;
                     }
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-                        for (int j = 0; j < NB; ++j) rr[j] += __shfl_xor_sync(0xffffffffu, rr[j], o);
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) rr[j] = rsqrtf(rr[j] / static_cast<float>(D) + p.norm_eps);
                 }
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    const int r = r0 + j;
-                    float f[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[j][i] << 16); f[2 * i + 1] = __uint_as_float(v[j][i] & 0xFFFF0000u); }
-                    if (p.q_norm_w)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = f[i] * rr[j] * nw[i];
-                    if (p.inv_freq && r < rows) {
-                        const int tk = (T.r0 + rbase + r) / p.H;
-                        if (tk != tok) { tok = tk; cs = rope_cs(p.inv_freq, lane, T.ctx + tk); }
+                if (p.inv_freq) {
+                    const int tk = (T.r0 + rbase + w0 + r) / p.H;
+                    if (tk != tok) {                 // a new token: lane i works out pair i, the RoPE lanes collect theirs
+                        tok = tk;
+                        const float2 mine = rope_cs(p.inv_freq, lane, T.ctx + tk);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int pair = ((lane * 16 - DN) / 2 + i) & 31;
-                            const float x = __shfl_sync(0xffffffffu, cs.x, pair), y = __shfl_sync(0xffffffffu, cs.y, pair);
-                            if (lane * 16 >= DN) {
-                                const float a = f[2 * i], b = f[2 * i + 1];
-                                f[2 * i] = a * x - b * y;
-                                f[2 * i + 1] = a * y + b * x;
-                            }
+                            cs[i].x = __shfl_sync(0xffffffffu, mine.x, pair);
+                            cs[i].y = __shfl_sync(0xffffffffu, mine.y, pair);
                         }
                     }
-                    uint8_t* blk = smem + Q_OFF + (lane >> 2) * 8192;
-                    const int ch = (lane & 3) * 2;
-                    *reinterpret_cast<uint4*>(blk + sw128(r, ch)) =
-                        make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-                    *reinterpret_cast<uint4*>(blk + sw128(r, ch + 1)) =
-                        make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
+                    if (lane * 16 >= DN)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float a = f[2 * i], b = f[2 * i + 1];
+                            f[2 * i] = a * cs[i].x - b * cs[i].y;
+                            f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
+                        }
                 }
+                *c0 = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                *c1 = make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
             }
             fence_async();
             __syncwarp();
@@ -625,13 +648,13 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         for (int kk = 0;; ++kk) {
             // one warp takes the item for all eight (they meet at barriers: all go on, or none)
             if (warp == 0) {
-                const int it = take_item(kk);
-                if (lane == 0) c.soft_item = it;
+                take_item(kk, I);
+                if (lane == 0) c.soft_item = I;
             }
             bar_sync(5, NSOFT * 32);
-            const int it = c.soft_item;
+            I = c.soft_item;
+            const int it = I.index;
             if (it < 0) break;
-            make_item(p, s, it, I);
             const Tile& T = I.T;
             const int n = I.n;
             const int rows = min(max(T.rows - rbase, 0), ROWS);
@@ -762,9 +785,9 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             bar_sync(5, NSOFT * 32);
             fence_after();
             const float m_used = c.m[(n - 1) & 1][r];
-            c.l[hk * 2 + g][r] = m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_used);
+            c.mx[g][hk][r] = m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_used);
             bar_sync(5, NSOFT * 32);
-            float l = c.l[0][r] + c.l[1][r] + c.l[2][r] + c.l[3][r];
+            float l = c.mx[0][0][r] + c.mx[0][1][r] + c.mx[1][0][r] + c.mx[1][1][r];
             const bool parts = p.n_splits > 1;
             if (parts && hk == 0 && g == 0) {
                 float* ml = p.part_ml + static_cast<int64_t>(it) * 2 * PAIR + rbase + r;
@@ -798,18 +821,16 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
 #pragma unroll
                     for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
                     if (rot && q2 == 1) {
+                        if (!one_tok) {
+                            rope_back_rows(f, p.inv_freq, q * 16, T.ctx + tok);
+                        } else {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float2 z;
-                            if (one_tok) {
-                                z.x = __shfl_sync(0xffffffffu, cs.x, q * 16 + j);
-                                z.y = __shfl_sync(0xffffffffu, cs.y, q * 16 + j);
-                            } else {
-                                z = rope_cs(p.inv_freq, q * 16 + j, T.ctx + tok);
+                            for (int j = 0; j < 16; ++j) {
+                                const float zx = __shfl_sync(0xffffffffu, cs.x, q * 16 + j), zy = __shfl_sync(0xffffffffu, cs.y, q * 16 + j);
+                                const float x = f[2 * j], y = f[2 * j + 1];
+                                f[2 * j] = x * zx + y * zy;
+                                f[2 * j + 1] = y * zx - x * zy;
                             }
-                            const float x = f[2 * j], y = f[2 * j + 1];
-                            f[2 * j] = x * z.x + y * z.y;
-                            f[2 * j + 1] = y * z.x - x * z.y;
                         }
                     }
 #pragma unroll
