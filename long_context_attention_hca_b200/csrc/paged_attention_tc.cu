@@ -23,9 +23,12 @@
 //
 // Per 128-key tile and CTA: 48 instructions, 2048 clocks at the tensor pipe's
 // rate; shared memory moves 256 KB for QK's operands (1024 clocks at 128 B), 96
-// KB for PV's (768) and 128 KB in.  The K and V parts of a tile are separate
-// 16 KB pieces of one ring of 8, consumed in the order QK(0), QK(i + 1), PV(i),
-// ...: the softmax of tile i runs beside QK(i + 1).
+// KB for PV's (768) and 128 KB in.  The K and the V part of a tile arrive as four
+// 16 KB pieces each, every piece with its own slot, so that a piece of the next
+// tile is on its way as soon as its predecessor is multiplied; one TMA a piece
+// and one issuing thread for K and one for V (one thread for both, four copies a
+// piece, spent 3.3K clocks a tile on issuing).  The softmax of tile i runs beside
+// QK(i + 1).
 //
 // The pairs are persistent: the grid is one pair per two SMs, and a pair takes
 // (tile, split of its keys) items from a counter until none is left, so that an
@@ -34,9 +37,9 @@
 // steps of few rows: their partial outputs are joined by the combine kernel.
 //
 // Warps: 0-7 softmax and output (two groups of four, tiles in turn; a row of a
-// tile is shared by two threads, one TMEM lane each), 8 TMA (in the first CTA
-// also the item counter), 9 QK issue, 10 PV issue (the first CTA's only), 11-14
-// query rows to fp16.  The online softmax is in base 2; O is rescaled only when
+// tile is shared by two threads, one TMEM lane each), 8 K copies (in the first
+// CTA also the item counter), 9 QK issue, 10 PV issue (the first CTA's only),
+// 11-14 query rows to fp16, 15 V copies.  The online softmax is in base 2; O is rescaled only when
 // a row's maximum grows by more than 2^8 (P <= 2^8 in fp16).  Every wait is
 // bounded: one that gives up sets the device error word, the CTA's outputs
 // become NaN, and the pair still meets at the end.
@@ -55,13 +58,13 @@ constexpr int D = 512;
 constexpr int PAIR = 128;                    // rows of a CTA pair
 constexpr int ROWS = 64;                     // rows of one CTA
 constexpr int HALF = 64;                     // keys of a half tile (one CTA's K)
-constexpr int NSLOT = 8, SLOT = 16384;
+constexpr int NSLOT = 8, SLOT = 16384;       // K pieces 0-3, V pieces 4-7
 constexpr int Q_OFF = 0;                     // 8 column blocks (64 dims) of 64 rows x 128 B
 constexpr int P_OFF = 65536;                 // 2 buffers of 2 column blocks (64 keys) of 64 rows x 128 B
 constexpr int R_OFF = P_OFF + 2 * 16384;
 constexpr int CTRL_OFF = R_OFF + NSLOT * SLOT;
 constexpr int SMEM = 232448;                 // all that a CTA may have: the rest is Ctrl's
-constexpr int NSOFT = 8, NQ = 4, NTHREADS = (11 + NQ) * 32;
+constexpr int NSOFT = 8, NQ = 4, NTHREADS = (12 + NQ) * 32;
 constexpr uint32_t S_COL = 0, O_COL = 128, TMEM_COLS = 512;
 constexpr float GROW = 8.0f;                 // log2 units
 constexpr int DR = 64, DN = D - DR;
@@ -192,11 +195,12 @@ __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
-// a tile of the staged rows into this CTA, its bytes counted at the barrier of the pair's first CTA
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar_first) {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-                 "[%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar_first) : "memory");
+// staged rows into this CTA, 64-dim column blocks one after the other, the bytes counted at the barrier of the pair's
+// first CTA
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int row, int block, uint32_t bar_first) {
+    asm volatile("cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                 "[%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(block), "r"(bar_first) : "memory");
 }
 __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
@@ -268,10 +272,6 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
     return true;
 }
 
-// ring position of piece 0 of K(i) and V(i): K(0), then K(i + 1), V(i) in turn
-__device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 8 * i - 4; }
-__device__ __forceinline__ int v_pos(int i, int n) { return i == n - 1 ? 8 * i + 4 : 8 * i + 8; }
-
 // One item: a tile's rows and the key tiles [k0, k0 + n) of its split.
 struct Item {
     Tile T;
@@ -293,8 +293,8 @@ struct Ctrl {
 };
 static_assert(CTRL_OFF + sizeof(Ctrl) <= SMEM, "shared memory");
 // warps that take an item from the mailbox: softmax (one for all), QK, PV and the query warps of the first CTA;
-// softmax, TMA and the query warps of the second
-constexpr int TAKERS = 3 + NQ + 2 + NQ;
+// softmax, K and the query warps of the second; V of both
+constexpr int TAKERS = 3 + NQ + 2 + NQ + 2;
 
 __device__ __forceinline__ bool make_item(const Params& p, const Stage& s, int item, Item& I) {
     const int t = item / p.n_splits, split = item - t * p.n_splits;
@@ -310,6 +310,30 @@ __device__ __forceinline__ bool make_item(const Params& p, const Stage& s, int i
     I.ent0 = rg.base;
     I.tok0 = rg.base + rg.n_e64;
     I.win0 = I.tok0 + rg.f + (I.T.w_lo - rg.w0);
+    return true;
+}
+
+// One thread: the four pieces of a key tile's K (slots 0-3, dims 128 j .., all rows from y) or V (slots 4-7, 32 keys
+// each: rows y, y + 32 of the tile's first half, y2, y2 + 32 of its second; dims of column blocks from `block`).  u: key
+// tiles before.  Waits for each slot, announces both CTAs' bytes (first CTA), copies.
+__device__ __forceinline__ bool copy_pieces(Ctrl& c, int slot0, int u, bool first, uint32_t dst, const CUtensorMap* map, int y,
+                                            int blocks, volatile int* abort_flag, int y2, int block) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t full = smem_u32(&c.full[slot0 + j]), empty = smem_u32(&c.empty[slot0 + j]);
+        if (u > 0 && !mbar_try(empty, (u - 1) & 1)) {
+            const long long t0 = clock64();
+            while (!mbar_try(empty, (u - 1) & 1))
+                if (*abort_flag || clock64() - t0 >= WAIT_CLOCKS) {
+                    *abort_flag = 1;
+                    atomicExch(&g_paged_device_error, 1);
+                    return false;
+                }
+        }
+        if (first) mbar_expect(full, 2 * SLOT);
+        if (blocks == 2) tma_3d(dst + j * SLOT, map, y, 2 * j, in_first(full));
+        else tma_3d(dst + j * SLOT, map, (j & 2 ? y2 : y) + (j & 1) * 32, block, in_first(full));
+    }
     return true;
 }
 
@@ -389,7 +413,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
     };
 
     if (warp == 8) {
-        // ------------------------------------------------------------ TMA, items
+        // ------------------------------------------------------------ K copies, items
         const bool leader = elect_one();
         // the next item with rows and keys, posted to both CTAs: where and how much is worked out once, here
         auto post_next = [&](int k, Item& J) {
@@ -431,60 +455,52 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             __syncwarp();
         };
         Item I, J;
-        int base = 0;
+        int u = 0;                                   // key tiles so far: each uses every K slot once
         if (rank == 0) post_next(0, I); else take_item(0, I);
         for (int k = 0; I.index >= 0 && ok; ++k) {
-            auto piece = [&](int pos) -> uint32_t {  // waits for the ring slot, announces both CTAs' bytes
-                const int sl = pos % NSLOT;
-                if (pos >= NSLOT && ok) ok = wait_bar(smem_u32(&c.empty[sl]), ((pos / NSLOT) & 1) ^ 1, abort_flag);
-                if (ok && rank == 0 && leader) mbar_expect(smem_u32(&c.full[sl]), 2 * SLOT);
-                return sbase + R_OFF + sl * SLOT;
-            };
-            for (int i = 0; i <= I.n && ok; ++i) {
-                if (i < I.n) {
-                    const int y = static_cast<int>(half_row(I, 2 * (I.k0 + i) + rank));
-                    for (int j = 0; j < 4 && ok; ++j) {
-                        const int pos = base + k_pos(i) + j;
-                        const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
-                        if (ok && leader) {
-                            tma_2d(dst, &k_map, j * 128, y, bar);
-                            tma_2d(dst + 8192, &k_map, j * 128 + 64, y, bar);
-                        }
-                    }
-                }
+            for (int i = 0; i < I.n && ok; ++i, ++u) {
+                const int y = static_cast<int>(half_row(I, 2 * (I.k0 + i) + rank));
+                if (leader) ok = copy_pieces(c, 0, u, rank == 0, sbase + R_OFF, &k_map, y, 2, abort_flag, 0, 0);
+                ok = __all_sync(0xffffffffu, ok);
                 if (i == 0 && rank == 0 && ok) post_next(k + 1, J);      // behind the item's first keys
-                if (i > 0) {
-                    for (int j = 0; j < 4 && ok; ++j) {
-                        const int pos = base + v_pos(i - 1, I.n) + j;
-                        const int y = static_cast<int>(half_row(I, 2 * (I.k0 + i - 1) + (j >> 1))) + (j & 1) * 32;
-                        const uint32_t dst = piece(pos), bar = in_first(smem_u32(&c.full[pos % NSLOT]));
-                        if (ok && leader)
-#pragma unroll
-                            for (int b = 0; b < 4; ++b) tma_2d(dst + b * 4096, &v_map, rank * 256 + b * 64, y, bar);
-                    }
-                }
             }
-            base += 8 * I.n;
             if (rank == 0) I = J; else take_item(k + 1, I);
         }
         // gave up: copies in flight land within microseconds, before this CTA's memory may go to another
+        if (!ok) for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    } else if (warp == 15) {
+        // ------------------------------------------------------------ V copies
+        const bool leader = elect_one();
+        Item I;
+        int u = 0;
+        for (int k = 0; ok; ++k) {
+            if (!take_item(k, I)) break;
+            for (int i = 0; i < I.n && ok; ++i, ++u) {
+                // keys 32 j .. of the tile: half tile j / 2, its rows 32 (j & 1) ..
+                const int h = 2 * (I.k0 + i);
+                if (leader)
+                    ok = copy_pieces(c, 4, u, rank == 0, sbase + R_OFF + 4 * SLOT, &v_map, static_cast<int>(half_row(I, h)), 4,
+                                     abort_flag, static_cast<int>(half_row(I, h + 1)), rank * 4);
+                ok = __all_sync(0xffffffffu, ok);
+            }
+        }
         if (!ok) for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else if (warp == 9 && rank == 0) {
         // ------------------------------------------------------------ QK issue
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_f16(128, 128, 0);
         const uint64_t qd = sdesc(sbase + Q_OFF, 16, 1024);
-        int base = 0, uses[2] = {0, 0};              // ring position; S buffers used so far
+        int u = 0, uses[2] = {0, 0};                 // key tiles and uses of each S buffer so far
         Item I;
         for (int k = 0; ok; ++k) {
             if (!take_item(k, I)) break;
             ok = wait_bar(smem_u32(&c.q_full), k & 1, abort_flag);
-            for (int i = 0; i < I.n && ok; ++i) {
+            for (int i = 0; i < I.n && ok; ++i, ++u) {
                 const int b = i & 1, use = (b ? uses[1] : uses[0]) + (i >> 1);
                 if (use > 0) ok = wait_bar(smem_u32(&c.s_free[b]), (use - 1) & 1, abort_flag);     // S's last use has been read
                 for (int j = 0; j < 4 && ok; ++j) {
-                    const int pos = base + k_pos(i) + j, sl = pos % NSLOT;
-                    ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
+                    const int sl = j;
+                    ok = wait_bar(smem_u32(&c.full[sl]), u & 1, abort_flag);
                     if (!ok) break;
                     fence_after();
                     const uint64_t kd = sdesc(sbase + R_OFF + sl * SLOT, 16, 1024);
@@ -500,7 +516,6 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     __syncwarp();
                 }
             }
-            base += 8 * I.n;
             uses[0] += (I.n + 1) / 2;
             uses[1] += I.n / 2;
         }
@@ -510,17 +525,17 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const bool leader = elect_one();
         constexpr uint32_t id = idesc_f16(128, 256, 1);
         const uint64_t pd = sdesc(sbase + P_OFF, 16, 1024);
-        int base = 0, uses[2] = {0, 0};
+        int u = 0, uses[2] = {0, 0};
         Item I;
         for (int k = 0; ok; ++k) {
             if (!take_item(k, I)) break;
             if (k > 0) ok = wait_bar(smem_u32(&c.o_free), (k - 1) & 1, abort_flag);               // O of the item before is out
-            for (int i = 0; i < I.n && ok; ++i) {
+            for (int i = 0; i < I.n && ok; ++i, ++u) {
                 const int b = i & 1, use = (b ? uses[1] : uses[0]) + (i >> 1);
                 ok = wait_bar(smem_u32(&c.p_full[b]), use & 1, abort_flag);
                 for (int j = 0; j < 4 && ok; ++j) {
-                    const int pos = base + v_pos(i, I.n) + j, sl = pos % NSLOT;
-                    ok = wait_bar(smem_u32(&c.full[sl]), (pos / NSLOT) & 1, abort_flag);
+                    const int sl = 4 + j;
+                    ok = wait_bar(smem_u32(&c.full[sl]), u & 1, abort_flag);
                     if (!ok) break;
                     fence_after();
                     // V: dims are contiguous (MN-major), 64-dim column blocks 4096 B apart, 8 keys 1024 B
@@ -541,7 +556,6 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     __syncwarp();
                 }
             }
-            base += 8 * I.n;
             uses[0] += (I.n + 1) / 2;
             uses[1] += I.n / 2;
         }
@@ -555,6 +569,12 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         uint8_t* const my = smem + Q_OFF + (lane >> 2) * 8192;       // dims 16 lane .. + 15: two chunks of column block lane / 4
         const int ch = (lane & 3) * 2;
         const uint32_t q_first = in_first(smem_u32(&c.q_full));
+        // (in registers: with all of the SM's memory shared there is no L1 to speak of, and a load of the weights per
+        // row cost 0.7K clocks each)
+        float nw[16];
+        if (p.q_norm_w)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) nw[i] = __ldg(p.q_norm_w + lane * 16 + i);
         Item I;
         for (int k = 0; ok; ++k) {
             if (!take_item(k, I)) break;
@@ -600,10 +620,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
                     const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
 #pragma unroll
-                    for (int i = 0; i < 16; i += 4) {
-                        const float4 nw = __ldg(reinterpret_cast<const float4*>(p.q_norm_w + lane * 16 + i));
-                        f[i] *= rr * nw.x; f[i + 1] *= rr * nw.y; f[i + 2] *= rr * nw.z; f[i + 3] *= rr * nw.w;
-                    }
+                    for (int i = 0; i < 16; ++i) f[i] = f[i] * rr * nw[i];
                 }
                 if (p.inv_freq) {
                     const int tk = (T.r0 + rbase + w0 + r) / p.H;
@@ -887,13 +904,14 @@ static EncodeTiledFn encode_fn() {
     return fn;
 }
 
-static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box_rows) {
+// The staged rows as [column block of 64 dims][row][64]: a copy of several blocks lays them one after the other.
+static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box_rows, uint32_t box_blocks) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    const cuuint64_t dim[2] = {D, static_cast<cuuint64_t>(bound)};
-    const cuuint64_t stride[1] = {D * 2};
-    const cuuint32_t box[2] = {64, box_rows}, ones[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, rows, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint64_t dim[3] = {64, static_cast<cuuint64_t>(bound), D / 64};
+    const cuuint64_t stride[2] = {D * 2, 128};
+    const cuuint32_t box[3] = {64, box_rows, box_blocks}, ones[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, rows, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -917,7 +935,7 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
     s.next = reinterpret_cast<int*>(s.flags + ((s.bound + 15) & ~int64_t(15)));
     s.n_items = static_cast<int>(tiles * p.n_splits);
     CUtensorMap km, vm;
-    if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF) || !tcp::make_map(&vm, s.rows, s.bound, 32)) return HCA_ERR_CUDA;
+    if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF, 2) || !tcp::make_map(&vm, s.rows, s.bound, 32, 4)) return HCA_ERR_CUDA;
     cudaError_t e = cudaFuncSetAttribute(tcp::paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcp::SMEM);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound, 8)), 256, 0, st>>>(p, s);
