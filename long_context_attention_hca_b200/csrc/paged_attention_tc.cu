@@ -185,14 +185,21 @@ __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
 }
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
     uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
                  "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
     return ok != 0;
 }
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" :: "r"(bar), "r"(bytes) : "memory");
 }
+// Arrival at a barrier of either CTA.  What it announces (operands in this CTA's shared memory, TMEM that has been read)
+// is ordered by the proxy and tcgen05 fences in front of it; a release at cluster scope would wait for every memory
+// operation of the thread, 1-2K clocks each time.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
+}
+// ... and one that publishes this thread's plain stores to the other CTA
+__device__ __forceinline__ void mbar_arrive_release(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(cluster_addr) : "memory");
 }
 // staged rows into this CTA, 64-dim column blocks one after the other, the bytes counted at the barrier of the pair's
@@ -406,9 +413,10 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
     // item k from the mailbox (false: no more); whole warps
     auto take_item = [&](int k, Item& I) -> bool {
         if (!wait_bar(smem_u32(&c.item_full[k & 1]), (k >> 1) & 1, abort_flag)) { ok = false; I.index = -1; return false; }
+        asm volatile("fence.acq_rel.cluster;" ::: "memory");       // the words came from the first CTA
         I = c.item[k & 1];
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.item_free[k & 1])));
+        if (lane == 0) mbar_arrive_release(in_first(smem_u32(&c.item_free[k & 1])));
         return I.index >= 0;
     };
 
@@ -450,7 +458,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             if (lane < 2) {
                 uint32_t bar;
                 asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(bar) : "r"(smem_u32(&c.item_full[k & 1])), "r"(lane));
-                mbar_arrive_cluster(bar);
+                mbar_arrive_release(bar);
             }
             __syncwarp();
         };
