@@ -294,7 +294,7 @@ struct Ctrl {
     Item item[2];
     float mx[2][2][ROWS];       // [group][key half][row]: a tile's largest raw logit; at the end each thread's l
     float m[2][ROWS];           // [tile parity]: the running maximum (base 2) after the tile
-    Item soft_item;             // the softmax warps' copy
+    Item soft_item[2];          // the softmax warps' copy, by item parity
     uint32_t tmem;
     int abort_flag;
 };
@@ -669,15 +669,19 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const uint32_t p_first = in_first(smem_u32(&c.p_full[g])), s_first = in_first(smem_u32(&c.s_free[g]));
         const uint32_t o_first = in_first(smem_u32(&c.o_free));
         int uses[2] = {0, 0};                        // of each parity's buffers, so far
-        Item I;
-        for (int kk = 0;; ++kk) {
-            // one warp takes the item for all eight (they meet at barriers: all go on, or none)
+        // one warp takes an item for all eight (they meet at barriers: all go on, or none), the next one ahead of the
+        // output of this one: the fence in there would wait for the output's stores
+        auto take_for_all = [&](int k) {
             if (warp == 0) {
-                take_item(kk, I);
-                if (lane == 0) c.soft_item = I;
+                Item J;
+                take_item(k, J);
+                if (lane == 0) c.soft_item[k & 1] = J;
             }
-            bar_sync(5, NSOFT * 32);
-            I = c.soft_item;
+        };
+        take_for_all(0);
+        bar_sync(5, NSOFT * 32);
+        for (int kk = 0;; ++kk) {
+            const Item I = c.soft_item[kk & 1];
             const int it = I.index;
             if (it < 0) break;
             const Tile& T = I.T;
@@ -697,6 +701,21 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             flags_of(g);
             for (int i = g; i < n; i += 2) {
                 const int h = 2 * (I.k0 + i) + hk, use = uses[g] + (i >> 1);
+                if (ok) ok = wait_bar(smem_u32(&c.s_full[g]), use & 1, abort_flag);
+                fence_after();
+                float v[64];
+                {
+                    uint32_t sr[32];
+                    tmem_ld32(lb + S_COL + g * 64, sr);
+                    uint32_t s2[32];
+                    tmem_ld32(lb + S_COL + g * 64 + 32, s2);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) { v[j] = __uint_as_float(sr[j]); v[32 + j] = __uint_as_float(s2[j]); }
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(s_first);            // S may be overwritten
                 // keys that this row sees among the half tile's 64, as bits
                 auto below = [](int k) -> unsigned { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
                 unsigned vis[2], bad = 0;
@@ -715,21 +734,6 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     bad |= vis[z] & nf;
                 }
                 flags_of(i + 2);
-                if (ok) ok = wait_bar(smem_u32(&c.s_full[g]), use & 1, abort_flag);
-                fence_after();
-                float v[64];
-                {
-                    uint32_t sr[32];
-                    tmem_ld32(lb + S_COL + g * 64, sr);
-                    uint32_t s2[32];
-                    tmem_ld32(lb + S_COL + g * 64 + 32, s2);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) { v[j] = __uint_as_float(sr[j]); v[32 + j] = __uint_as_float(s2[j]); }
-                }
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(s_first);            // S may be overwritten
                 if (!__all_sync(0xffffffffu, (vis[0] & vis[1]) == 0xffffffffu))
 #pragma unroll
                     for (int j = 0; j < 64; ++j) v[j] = ((vis[j >> 5] >> (j & 31)) & 1u) ? v[j] : -INFINITY;
@@ -802,6 +806,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(p_first);
             }
+            take_for_all(kk + 1);
             // ---- the item's output.  The last tile's group waits for the last PV (it has seen the phase before; the
             // other group may not have)
             if (g == ((n - 1) & 1) && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (uses[g] + ((n - 1) >> 1)) & 1, abort_flag);
@@ -874,9 +879,17 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 bar_sync(5, NSOFT * 32);
                 uint16_t* dst = parts ? p.part_o + (static_cast<int64_t>(it) * PAIR + rbase) * D : p.out + (T.row0 + rbase) * D;
                 // lane = (segment, chunk): dims 128 segment + 64 q2 + 8 chunk
-                for (int rr = warp; rr < rows; rr += NSOFT)
-                    *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(rr) * D + (lane >> 3) * 128 + q2 * 64 + (lane & 7) * 8) =
-                        *reinterpret_cast<const uint4*>(ob + rr * 512 + ((lane ^ (rr & 7)) << 4));
+                uint4 seg[ROWS / NSOFT];
+#pragma unroll
+                for (int j = 0; j < ROWS / NSOFT; ++j) {
+                    const int rr = warp + j * NSOFT;
+                    seg[j] = *reinterpret_cast<const uint4*>(ob + rr * 512 + ((lane ^ (rr & 7)) << 4));
+                }
+#pragma unroll
+                for (int j = 0; j < ROWS / NSOFT; ++j)
+                    if (warp + j * NSOFT < rows)
+                        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(warp + j * NSOFT) * D + (lane >> 3) * 128 + q2 * 64 +
+                                                  (lane & 7) * 8) = seg[j];
                 bar_sync(5, NSOFT * 32);
             }
         }
