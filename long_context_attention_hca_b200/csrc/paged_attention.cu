@@ -17,7 +17,7 @@ namespace hca {
 namespace paged {
 
 int64_t tc_stage_rows(int64_t n_rows, int B, int64_t max_entries, int W, int n_first);
-size_t tc_stage_bytes(int64_t rows);
+size_t tc_stage_bytes(int64_t rows, int64_t n_rows);
 int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* ws, cudaStream_t st);
 
 // ---------------------------------------------------------------- row kernel
@@ -589,7 +589,7 @@ static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int6
     // tiles that can hold rows: one a request when no request fills more
     const int64_t busy = max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs;
     if (k.pairs) {
-        k.stage_bytes = tc_stage_bytes(stage_rows);
+        k.stage_bytes = tc_stage_bytes(stage_rows, n_rows);
         k.splits = split_count(sm_count() / 2, busy, max_keys, 128, 2);
     } else {
         k.splits = split_count(sm_count(), busy, max_keys, TK, 2);

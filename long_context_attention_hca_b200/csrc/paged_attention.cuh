@@ -56,19 +56,24 @@ __device__ __forceinline__ int64_t tile0(const Params& p, int b, int R) {
     return static_cast<int64_t>(p.row_start[b]) * p.H / R + b;
 }
 
-__device__ __forceinline__ int find_tile_req(const Params& p, int64_t t, int R) {
+// The largest b in [0, n) with at_most(b), which holds up to some b >= 0 and for
+// none after; whole warps.
+template <class F>
+__device__ __forceinline__ int last_at_most(int n, F at_most) {
     const int lane = threadIdx.x & 31;
-    int lo = 0, hi = p.B;
+    int lo = 0, hi = n;
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
         const int c = lo + lane * step;
-        const bool le = c < hi && (c == 0 || tile0(p, c, R) <= t);
-        const unsigned mask = __ballot_sync(0xffffffffu, le);
-        const int k = mask ? 31 - __clz(mask) : 0;
-        lo += k * step;
+        const unsigned mask = __ballot_sync(0xffffffffu, c < hi && (lane == 0 || at_most(c)));
+        lo += (31 - __clz(mask)) * step;
         if (lo + step < hi) hi = lo + step;
     }
     return lo;
+}
+
+__device__ __forceinline__ int find_tile_req(const Params& p, int64_t t, int R) {
+    return last_at_most(p.B, [&](int b) { return tile0(p, b, R) <= t; });
 }
 
 // One tile's rows and keys.  Key slots in order: entries [0, n_e), first

@@ -75,6 +75,7 @@ struct Stage {
     uint8_t* flags;             // [bound]: 1 not visible, 2 non-finite
     int64_t per_req;            // rows of a request besides its new tokens
     int64_t bound;              // rows of the workspace
+    float2* cs;                 // [n_rows][32]: cos / sin of each new token's RoPE pairs (with inv_freq)
     int* next;                  // the item counter
     int n_items;                // tiles x splits
 };
@@ -105,18 +106,16 @@ __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
     const int64_t g = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     pdl_trigger();                              // the attention's prologue may start
     if (g == 0 && lane == 0) *s.next = 0;
-    if (g >= s.bound) return;
-    // largest b with b per_req + row_start[b] <= g, 32 candidates a round
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32;
-        const int c = lo + lane * step;
-        const bool le = c < hi && (c == lo || c * s.per_req + p.row_start[c] <= g);
-        const unsigned mask = __ballot_sync(0xffffffffu, le);
-        lo += (31 - __clz(mask)) * step;
-        if (lo + step < hi) hi = lo + step;
+    if (g >= s.bound) {
+        // a new token's RoPE table, lane = pair: once here, where every row's conversion and output would go through
+        // sincos again (7K clocks an item there, most of them instruction fetches)
+        const int64_t n = g - s.bound;
+        if (p.inv_freq == nullptr || n >= p.n_rows || n >= p.row_start[p.B]) return;
+        const int b = last_at_most(p.B, [&](int c) { return p.row_start[c] <= n; });
+        s.cs[n * 32 + lane] = rope_cs(p.inv_freq, lane, (p.ctx[b] > 0 ? p.ctx[b] : 0) + n - p.row_start[b]);
+        return;
     }
-    const int b = lo;
+    const int b = last_at_most(p.B, [&](int c) { return c * s.per_req + p.row_start[c] <= g; });
     const int64_t st = p.row_start[b];
     const int64_t en = p.row_start[b + 1] < p.n_rows ? p.row_start[b + 1] : p.n_rows;
     const int n_new = st < 0 || en < st ? 0 : static_cast<int>(en - st);
@@ -286,6 +285,7 @@ struct Item {
     int k0, n;
     int h_e, h_f, n_half;       // half tiles of 64 staged rows: entries, first tokens, all
     int64_t ent0, tok0, win0;   // staged rows of the first entry, first token, first window token
+    int64_t tok_row;            // row of the request's first new token
 };
 
 struct Ctrl {
@@ -315,6 +315,7 @@ __device__ __forceinline__ bool make_item(const Params& p, const Stage& s, int i
     I.k0 = static_cast<int>(static_cast<int64_t>(tiles) * split / p.n_splits);
     I.n = static_cast<int>(static_cast<int64_t>(tiles) * (split + 1) / p.n_splits) - I.k0;
     I.ent0 = rg.base;
+    I.tok_row = p.row_start[I.T.b];
     I.tok0 = rg.base + rg.n_e64;
     I.win0 = I.tok0 + rg.f + (I.T.w_lo - rg.w0);
     return true;
@@ -349,26 +350,6 @@ __device__ __forceinline__ int64_t half_row(const Item& I, int h) {
     if (h < I.h_e) return I.ent0 + h * HALF;
     if (h < I.h_e + I.h_f) return I.tok0 + (h - I.h_e) * HALF;
     return h < I.n_half ? I.win0 + (h - I.h_e - I.h_f) * HALF : I.win0;
-}
-
-// RoPE back of 32 dims (pairs pair0 ..) of a row whose neighbours in the warp are
-// other tokens' (few heads): rolled and out of line, to keep the usual path short.
-__device__ __noinline__ void rope_back_16(float* g, const float* inv_freq, int pair0, int64_t pos) {
-#pragma unroll 1
-    for (int j = 0; j < 16; ++j) {
-        const float2 z = rope_cs(inv_freq, pair0 + j, pos);
-        const float x = g[2 * j], y = g[2 * j + 1];
-        g[2 * j] = x * z.x + y * z.y;
-        g[2 * j + 1] = y * z.x - x * z.y;
-    }
-}
-__device__ __forceinline__ void rope_back_rows(float (&f)[32], const float* inv_freq, int pair0, int64_t pos) {
-    float g[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) g[j] = f[j];
-    rope_back_16(g, inv_freq, pair0, pos);
-#pragma unroll
-    for (int j = 0; j < 32; ++j) f[j] = g[j];
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
@@ -582,7 +563,8 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         float nw[16];
         if (p.q_norm_w)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) nw[i] = __ldg(p.q_norm_w + lane * 16 + i);
+            for (int i = 0; i < 16; ++i)             // (volatile: not to be loaded again in the loop)
+                asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(nw[i]) : "l"(p.q_norm_w + lane * 16 + i));
         Item I;
         for (int k = 0; ok; ++k) {
             if (!take_item(k, I)) break;
@@ -609,49 +591,77 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 }
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
-            int tok = -1;
+            // token of a row, counted up: a division per item instead of one per row
+            int tok = (T.r0 + rbase + w0) / p.H, head = (T.r0 + rbase + w0) - tok * p.H, cs_tok = tok;
             float2 cs[8];                            // of this lane's pairs (lanes that hold RoPE dims), at the row's position
-#pragma unroll 1
-            for (int r = 0; r < ROWS / NQ && w0 + r < rows; ++r) {
-                uint4* c0 = reinterpret_cast<uint4*>(my + sw128(w0 + r, ch));
-                uint4* c1 = reinterpret_cast<uint4*>(my + sw128(w0 + r, ch + 1));
-                const uint4 a0 = *c0, a1 = *c1;
-                const uint32_t v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
-                float f[16];
+            auto load_cs = [&](int tk) {
+                if (lane * 16 >= DN && tk < T.n_new) {
+                    const float4* from = reinterpret_cast<const float4*>(s.cs + (I.tok_row + tk) * 32 + (lane * 16 - DN) / 2);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[i] << 16); f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u); }
-                if (p.q_norm_w) {
-                    float ss = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) ss += f[i] * f[i];
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    const float rr = rsqrtf(ss / static_cast<float>(D) + p.norm_eps);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) f[i] = f[i] * rr * nw[i];
-                }
-                if (p.inv_freq) {
-                    const int tk = (T.r0 + rbase + w0 + r) / p.H;
-                    if (tk != tok) {                 // a new token: lane i works out pair i, the RoPE lanes collect theirs
-                        tok = tk;
-                        const float2 mine = rope_cs(p.inv_freq, lane, T.ctx + tk);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int pair = ((lane * 16 - DN) / 2 + i) & 31;
-                            cs[i].x = __shfl_sync(0xffffffffu, mine.x, pair);
-                            cs[i].y = __shfl_sync(0xffffffffu, mine.y, pair);
-                        }
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 c2 = from[i];
+                        cs[2 * i] = make_float2(c2.x, c2.y);
+                        cs[2 * i + 1] = make_float2(c2.z, c2.w);
                     }
-                    if (lane * 16 >= DN)
+                }
+            };
+            if (p.inv_freq) load_cs(tok);
+            constexpr int NB = 4;                    // rows whose chains of operations run side by side
+#pragma unroll 1
+            for (int r = w0; r < w0 + ROWS / NQ && r < rows; r += NB) {      // (rows past the last are zeros: harmless)
+                uint32_t v[NB][8];
+                float rr[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(my + sw128(r + j, ch));
+                    *reinterpret_cast<uint4*>(v[j] + 4) = *reinterpret_cast<const uint4*>(my + sw128(r + j, ch + 1));
+                }
+                if (p.q_norm_w) {
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float a = f[2 * i], b = f[2 * i + 1];
-                            f[2 * i] = a * cs[i].x - b * cs[i].y;
-                            f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
+                            const float a = __uint_as_float(v[j][i] << 16), b = __uint_as_float(v[j][i] & 0xFFFF0000u);
+                            s0 += a * a;
+                            s1 += b * b;
                         }
+                        rr[j] = s0 + s1;
+                    }
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1)
+#pragma unroll
+                        for (int j = 0; j < NB; ++j) rr[j] += __shfl_xor_sync(0xffffffffu, rr[j], o);
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) rr[j] = rsqrtf(rr[j] * (1.0f / D) + p.norm_eps);
                 }
-                *c0 = make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-                *c1 = make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    float f[16];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[j][i] << 16); f[2 * i + 1] = __uint_as_float(v[j][i] & 0xFFFF0000u); }
+                    if (p.q_norm_w)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) f[i] = f[i] * rr[j] * nw[i];
+                    if (p.inv_freq) {
+                        if (tok != cs_tok) {
+                            cs_tok = tok;
+                            load_cs(tok);
+                        }
+                        if (lane * 16 >= DN)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float a = f[2 * i], b = f[2 * i + 1];
+                                f[2 * i] = a * cs[i].x - b * cs[i].y;
+                                f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
+                            }
+                    }
+                    *reinterpret_cast<uint4*>(my + sw128(r + j, ch)) =
+                        make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
+                    *reinterpret_cast<uint4*>(my + sw128(r + j, ch + 1)) =
+                        make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
+                    if (++head == p.H) { head = 0; ++tok; }
+                }
             }
             fence_async();
             __syncwarp();
@@ -831,7 +841,8 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             const bool rot = !parts && p.inv_freq && hk == 1 && g == 1;      // this warp holds the RoPE dims
             const bool one_tok = __all_sync(0xffffffffu, tok == __shfl_sync(0xffffffffu, tok, 0));
             float2 cs = make_float2(1.0f, 0.0f);
-            if (rot && one_tok) cs = rope_cs(p.inv_freq, lane, T.ctx + tok);
+            const float2* row_cs = s.cs + (I.tok_row + tok) * 32;
+            if (rot && one_tok) cs = row_cs[lane];
             // O: row r, dims 256 hk + 128 g .. + 127, half of them at a time through the P buffers (free now): 64 rows of
             // four 128-byte segments, one per (hk, g), 16-byte chunks swizzled by row; then whole segments out
             uint8_t* ob = smem + P_OFF;
@@ -851,16 +862,17 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
 #pragma unroll
                     for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
                     if (rot && q2 == 1) {
-                        if (!one_tok) {
-                            rope_back_rows(f, p.inv_freq, q * 16, T.ctx + tok);
-                        } else {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float zx = __shfl_sync(0xffffffffu, cs.x, q * 16 + j), zy = __shfl_sync(0xffffffffu, cs.y, q * 16 + j);
-                                const float x = f[2 * j], y = f[2 * j + 1];
-                                f[2 * j] = x * zx + y * zy;
-                                f[2 * j + 1] = y * zx - x * zy;
+                        for (int j = 0; j < 16; ++j) {
+                            float zx = __shfl_sync(0xffffffffu, cs.x, q * 16 + j), zy = __shfl_sync(0xffffffffu, cs.y, q * 16 + j);
+                            if (!one_tok) {              // few heads: the neighbours are other tokens' rows
+                                const float2 z = row_cs[q * 16 + j];
+                                zx = z.x;
+                                zy = z.y;
                             }
+                            const float x = f[2 * j], y = f[2 * j + 1];
+                            f[2 * j] = x * zx + y * zy;
+                            f[2 * j + 1] = y * zx - x * zy;
                         }
                     }
 #pragma unroll
@@ -938,28 +950,31 @@ static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box
 
 }  // namespace tcp
 
-// Workspace: staged rows (fp16), a flag byte a row, the item counter.
+// Workspace: staged rows (fp16), the new tokens' RoPE table, a flag byte a staged row, the item counter.
 static int64_t stage_per_req(int64_t max_entries, int W, int n_first) {
     return ((max_entries + 63) & ~int64_t(63)) + n_first + W + 63;
 }
 int64_t tc_stage_rows(int64_t n_rows, int B, int64_t max_entries, int W, int n_first) {
     return B * stage_per_req(max_entries, W, n_first) + n_rows;
 }
-size_t tc_stage_bytes(int64_t rows) { return (static_cast<size_t>(rows) * (tcp::D * 2 + 1) + 16 + 255) & ~size_t(255); }
+size_t tc_stage_bytes(int64_t rows, int64_t n_rows) {
+    return (static_cast<size_t>(rows) * (tcp::D * 2 + 1) + static_cast<size_t>(n_rows) * 256 + 32 + 255) & ~size_t(255);
+}
 
 int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* ws, cudaStream_t st) {
     tcp::Stage s;
     s.per_req = stage_per_req(max_entries, p.W, p.n_first);
     s.bound = tc_stage_rows(p.n_rows, p.B, max_entries, p.W, p.n_first);
     s.rows = static_cast<uint16_t*>(ws);
-    s.flags = reinterpret_cast<uint8_t*>(s.rows + s.bound * tcp::D);
+    s.cs = reinterpret_cast<float2*>(s.rows + s.bound * tcp::D);
+    s.flags = reinterpret_cast<uint8_t*>(s.cs + p.n_rows * 32);
     s.next = reinterpret_cast<int*>(s.flags + ((s.bound + 15) & ~int64_t(15)));
     s.n_items = static_cast<int>(tiles * p.n_splits);
     CUtensorMap km, vm;
     if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF, 2) || !tcp::make_map(&vm, s.rows, s.bound, 32, 4)) return HCA_ERR_CUDA;
     cudaError_t e = cudaFuncSetAttribute(tcp::paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcp::SMEM);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
-    tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound, 8)), 256, 0, st>>>(p, s);
+    tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound + (p.inv_freq ? p.n_rows : 0), 8)), 256, 0, st>>>(p, s);
     HCA_CHECK_LAUNCH();
     const int64_t pairs = sm_count() / 2 < s.n_items ? sm_count() / 2 : s.n_items;
     e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm);
