@@ -248,6 +248,10 @@ __device__ __forceinline__ void tmem_st32(uint32_t a, const uint32_t (&r)[32]) {
                     "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
                  : "memory");
 }
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* w) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
 // shared-memory matrix descriptor, 128-byte swizzle (sm_100 format)
 __device__ __forceinline__ uint64_t sdesc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
     return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
@@ -691,7 +695,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         take_for_all(0);
         bar_sync(5, NSOFT * 32);
         for (int kk = 0;; ++kk) {
-            const Item I = c.soft_item[kk & 1];
+            const Item& I = c.soft_item[kk & 1];     // (read where needed: its fields in registers would spill others)
             const int it = I.index;
             if (it < 0) break;
             const Tile& T = I.T;
@@ -843,66 +847,55 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             float2 cs = make_float2(1.0f, 0.0f);
             const float2* row_cs = s.cs + (I.tok_row + tok) * 32;
             if (rot && one_tok) cs = row_cs[lane];
-            // O: row r, dims 256 hk + 128 g .. + 127, half of them at a time through the P buffers (free now): 64 rows of
-            // four 128-byte segments, one per (hk, g), 16-byte chunks swizzled by row; then whole segments out
-            uint8_t* ob = smem + P_OFF;
+            bar_sync(5, NSOFT * 32);                 // c.mx is read: the next item may write it
+            // O: row r, dims 256 hk + 128 g .. + 127 straight from registers, 32 bytes (a whole sector) a store where
+            // the output allows it (through shared memory, for stores of whole rows, took 5.3K clocks an item)
+            uint16_t* dst = (parts ? p.part_o + (static_cast<int64_t>(it) * PAIR + rbase) * D : p.out + (T.row0 + rbase) * D) +
+                            static_cast<int64_t>(r) * D + hk * 256 + g * 128;
+            const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;     // (the same for every row)
 #pragma unroll 1
-            for (int q2 = 0; q2 < 2; ++q2) {
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                tmem_ld32(lb + O_COL + g * 128 + q * 32, o);
+                tmem_wait_ld();
+                if (q == 3) {                        // O has been read
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(o_first);
+                }
+                float f[32];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t o[32];
-                    tmem_ld32(lb + O_COL + g * 128 + q2 * 64 + q * 32, o);
-                    tmem_wait_ld();
-                    if (q2 == 1 && q == 1) {             // O has been read
-                        fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(o_first);
-                    }
-                    float f[32];
+                for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
+                if (rot && q >= 2) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
-                    if (rot && q2 == 1) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float zx = __shfl_sync(0xffffffffu, cs.x, q * 16 + j), zy = __shfl_sync(0xffffffffu, cs.y, q * 16 + j);
-                            if (!one_tok) {              // few heads: the neighbours are other tokens' rows
-                                const float2 z = row_cs[q * 16 + j];
-                                zx = z.x;
-                                zy = z.y;
-                            }
-                            const float x = f[2 * j], y = f[2 * j + 1];
-                            f[2 * j] = x * zx + y * zy;
-                            f[2 * j + 1] = y * zx - x * zy;
+                    for (int j = 0; j < 16; ++j) {
+                        float zx = __shfl_sync(0xffffffffu, cs.x, (q & 1) * 16 + j), zy = __shfl_sync(0xffffffffu, cs.y, (q & 1) * 16 + j);
+                        if (!one_tok) {              // few heads: the neighbours are other tokens' rows
+                            const float2 z = row_cs[(q & 1) * 16 + j];
+                            zx = z.x;
+                            zy = z.y;
                         }
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float x = f[8 * j + 2 * k], y = f[8 * j + 2 * k + 1];
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
-                            w[k] = parts ? pack_half2(x, y) : *reinterpret_cast<const uint32_t*>(&b2);
-                        }
-                        const int ch = (hk * 2 + g) * 8 + q * 4 + j;
-                        *reinterpret_cast<uint4*>(ob + r * 512 + ((ch ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                        const float x = f[2 * j], y = f[2 * j + 1];
+                        f[2 * j] = x * zx + y * zy;
+                        f[2 * j + 1] = y * zx - x * zy;
                     }
                 }
-                bar_sync(5, NSOFT * 32);
-                uint16_t* dst = parts ? p.part_o + (static_cast<int64_t>(it) * PAIR + rbase) * D : p.out + (T.row0 + rbase) * D;
-                // lane = (segment, chunk): dims 128 segment + 64 q2 + 8 chunk
-                uint4 seg[ROWS / NSOFT];
+                uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < ROWS / NSOFT; ++j) {
-                    const int rr = warp + j * NSOFT;
-                    seg[j] = *reinterpret_cast<const uint4*>(ob + rr * 512 + ((lane ^ (rr & 7)) << 4));
+                for (int k = 0; k < 16; ++k) {
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
+                    w[k] = parts ? pack_half2(f[2 * k], f[2 * k + 1]) : *reinterpret_cast<const uint32_t*>(&b2);
                 }
+                if (r < rows) {
+                    if (wide) {
+                        st_global_32(dst + q * 32, w);
+                        st_global_32(dst + q * 32 + 16, w + 8);
+                    } else {
 #pragma unroll
-                for (int j = 0; j < ROWS / NSOFT; ++j)
-                    if (warp + j * NSOFT < rows)
-                        *reinterpret_cast<uint4*>(dst + static_cast<int64_t>(warp + j * NSOFT) * D + (lane >> 3) * 128 + q2 * 64 +
-                                                  (lane & 7) * 8) = seg[j];
-                bar_sync(5, NSOFT * 32);
+                        for (int k = 0; k < 4; ++k)
+                            *reinterpret_cast<uint4*>(dst + q * 32 + k * 8) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    }
+                }
             }
         }
         fence_before();
