@@ -223,6 +223,32 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
     return ok != 0;
 }
+// pairs of floats in one register pair (two operations an instruction)
+__device__ __forceinline__ uint64_t pair64(uint32_t lo, uint32_t hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -564,11 +590,11 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const uint32_t q_first = in_first(smem_u32(&c.q_full));
         // (in registers: with all of the SM's memory shared there is no L1 to speak of, and a load of the weights per
         // row cost 0.7K clocks each)
-        float nw[16];
+        uint64_t nw[8];
         if (p.q_norm_w)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)             // (volatile: not to be loaded again in the loop)
-                asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(nw[i]) : "l"(p.q_norm_w + lane * 16 + i));
+            for (int i = 0; i < 8; ++i)              // (volatile: not to be loaded again in the loop)
+                asm volatile("ld.global.nc.b64 %0, [%1];" : "=l"(nw[i]) : "l"(p.q_norm_w + lane * 16 + 2 * i));
         Item I;
         for (int k = 0; ok; ++k) {
             if (!take_item(k, I)) break;
@@ -610,62 +636,50 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 }
             };
             if (p.inv_freq) load_cs(tok);
-            constexpr int NB = 4;                    // rows whose chains of operations run side by side
+            // one warp issues an instruction every two or three clocks here, so the arithmetic is on pairs (f32x2)
 #pragma unroll 1
-            for (int r = w0; r < w0 + ROWS / NQ && r < rows; r += NB) {      // (rows past the last are zeros: harmless)
-                uint32_t v[NB][8];
-                float rr[NB];
+            for (int r = w0; r < w0 + ROWS / NQ && r < rows; ++r) {
+                uint4* const c0 = reinterpret_cast<uint4*>(my + sw128(r, ch));
+                uint4* const c1 = reinterpret_cast<uint4*>(my + sw128(r, ch + 1));
+                const uint4 a0 = *c0, a1 = *c1;
+                const uint32_t v[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+                uint64_t f[8];
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(my + sw128(r + j, ch));
-                    *reinterpret_cast<uint4*>(v[j] + 4) = *reinterpret_cast<const uint4*>(my + sw128(r + j, ch + 1));
-                }
+                for (int i = 0; i < 8; ++i) f[i] = pair64(v[i] << 16, v[i] & 0xFFFF0000u);
                 if (p.q_norm_w) {
+                    uint64_t s0 = 0, s1 = 0;
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        float s0 = 0.0f, s1 = 0.0f;
+                    for (int i = 0; i < 4; ++i) {
+                        s0 = fma2(f[i], f[i], s0);
+                        s1 = fma2(f[i + 4], f[i + 4], s1);
+                    }
+                    const float2 sa = unpair(s0), sb = unpair(s1);
+                    float ss = (sa.x + sa.y) + (sb.x + sb.y);
+#pragma unroll
+                    for (int o = 16; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    const float rr = rsqrtf(ss * (1.0f / D) + p.norm_eps);
+                    const uint64_t r2 = pair64(__float_as_uint(rr), __float_as_uint(rr));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) f[i] = mul2(mul2(f[i], r2), nw[i]);
+                }
+                if (p.inv_freq) {
+                    if (tok != cs_tok) {
+                        cs_tok = tok;
+                        load_cs(tok);
+                    }
+                    if (lane * 16 >= DN)
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            const float a = __uint_as_float(v[j][i] << 16), b = __uint_as_float(v[j][i] & 0xFFFF0000u);
-                            s0 += a * a;
-                            s1 += b * b;
+                            const float2 ab = unpair(f[i]);
+                            f[i] = pair64(__float_as_uint(ab.x * cs[i].x - ab.y * cs[i].y), __float_as_uint(ab.x * cs[i].y + ab.y * cs[i].x));
                         }
-                        rr[j] = s0 + s1;
-                    }
-#pragma unroll
-                    for (int o = 16; o >= 1; o >>= 1)
-#pragma unroll
-                        for (int j = 0; j < NB; ++j) rr[j] += __shfl_xor_sync(0xffffffffu, rr[j], o);
-#pragma unroll
-                    for (int j = 0; j < NB; ++j) rr[j] = rsqrtf(rr[j] * (1.0f / D) + p.norm_eps);
-                }
-#pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    float f[16];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) { f[2 * i] = __uint_as_float(v[j][i] << 16); f[2 * i + 1] = __uint_as_float(v[j][i] & 0xFFFF0000u); }
-                    if (p.q_norm_w)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) f[i] = f[i] * rr[j] * nw[i];
-                    if (p.inv_freq) {
-                        if (tok != cs_tok) {
-                            cs_tok = tok;
-                            load_cs(tok);
-                        }
-                        if (lane * 16 >= DN)
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const float a = f[2 * i], b = f[2 * i + 1];
-                                f[2 * i] = a * cs[i].x - b * cs[i].y;
-                                f[2 * i + 1] = a * cs[i].y + b * cs[i].x;
-                            }
-                    }
-                    *reinterpret_cast<uint4*>(my + sw128(r + j, ch)) =
-                        make_uint4(pack_half2(f[0], f[1]), pack_half2(f[2], f[3]), pack_half2(f[4], f[5]), pack_half2(f[6], f[7]));
-                    *reinterpret_cast<uint4*>(my + sw128(r + j, ch + 1)) =
-                        make_uint4(pack_half2(f[8], f[9]), pack_half2(f[10], f[11]), pack_half2(f[12], f[13]), pack_half2(f[14], f[15]));
                     if (++head == p.H) { head = 0; ++tok; }
                 }
+                uint32_t h[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) { const float2 ab = unpair(f[i]); h[i] = pack_half2(ab.x, ab.y); }
+                *c0 = make_uint4(h[0], h[1], h[2], h[3]);
+                *c1 = make_uint4(h[4], h[5], h[6], h[7]);
             }
             fence_async();
             __syncwarp();
@@ -778,18 +792,20 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 if (i + 1 < n) asm volatile("bar.arrive %0, 256;" :: "r"(3 + ((i + 1) & 1)) : "memory");
                 const float ref = m_new == -INFINITY ? 0.0f : m_new;
                 uint32_t pk[32];
-                float ps[16];
+                // l sums the probabilities in fp32 as they are; PV uses them rounded to fp16, which weighs a key by at
+                // most half a step (2^-11) more or less
+                uint64_t ps[4] = {0, 0, 0, 0};
+                const uint64_t sc2 = pair64(__float_as_uint(p.scale_log2), __float_as_uint(p.scale_log2));
+                const uint64_t rf2 = pair64(__float_as_uint(-ref), __float_as_uint(-ref));
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    pk[j] = pack_half2(ex2(fmaf(v[2 * j], p.scale_log2, -ref)), ex2(fmaf(v[2 * j + 1], p.scale_log2, -ref)));
-                    const float2 f = unpack_half2(pk[j]);    // l sums the probabilities as PV uses them
-                    if (j < 16) ps[j] = f.x + f.y; else ps[j - 16] += f.x + f.y;
+                    const float2 x = unpair(fma2(pair64(__float_as_uint(v[2 * j]), __float_as_uint(v[2 * j + 1])), sc2, rf2));
+                    const float e0 = ex2(x.x), e1 = ex2(x.y);
+                    pk[j] = pack_half2(e0, e1);
+                    ps[j & 3] = add2(ps[j & 3], pair64(__float_as_uint(e0), __float_as_uint(e1)));
                 }
-#pragma unroll
-                for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-                    for (int j = 0; j < w; ++j) ps[j] += ps[j + w];
-                l_run = (m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_new)) + ps[0];
+                const float2 pt = unpair(add2(add2(ps[0], ps[1]), add2(ps[2], ps[3])));
+                l_run = (m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_new)) + (pt.x + pt.y);
                 m_l = m_new;
                 if (bad) l_run = __int_as_float(0x7fc00000);             // a visible key that is not finite
                 if (use > 0 && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (use - 1) & 1, abort_flag);   // P's buffer is free
