@@ -208,6 +208,10 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
                  "[%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(dst), "l"(map), "r"(0), "r"(row), "r"(block), "r"(bar_first) : "memory");
 }
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 :: "l"(map), "r"(x), "r"(y), "r"(src) : "memory");
+}
 __device__ __forceinline__ void mma2(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                  "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}"
@@ -383,7 +387,8 @@ __device__ __forceinline__ int64_t half_row(const Item& I, int h) {
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NTHREADS, 1)
-paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map) {
+paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map,
+                const __grid_constant__ CUtensorMap o_map, const __grid_constant__ CUtensorMap p_map) {
     extern __shared__ __align__(1024) uint8_t smem[];
     Ctrl& c = *reinterpret_cast<Ctrl*>(smem + CTRL_OFF);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -864,10 +869,15 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             const float2* row_cs = s.cs + (I.tok_row + tok) * 32;
             if (rot && one_tok) cs = row_cs[lane];
             bar_sync(5, NSOFT * 32);                 // c.mx is read: the next item may write it
-            // O: row r, dims 256 hk + 128 g .. + 127 straight from registers, 32 bytes (a whole sector) a store where
-            // the output allows it (through shared memory, for stores of whole rows, took 5.3K clocks an item)
-            uint16_t* dst = (parts ? p.part_o + (static_cast<int64_t>(it) * PAIR + rbase) * D : p.out + (T.row0 + rbase) * D) +
-                            static_cast<int64_t>(r) * D + hk * 256 + g * 128;
+            // O: row r, dims 256 hk + 128 g .. + 127, half of them at a time.  64 rows (always, with 64 heads; partials
+            // always): through the P buffers (free now) as four blocks of 64 rows x 64 dims, 128-byte swizzle, each
+            // stored by one TMA copy.  Fewer rows: straight from registers, 32 bytes (a sector) a store where the output
+            // allows it (for all rows, that kept the load/store unit busy for 4K clocks an item, and the next item's
+            // query conversion waiting).
+            const bool whole = parts || rows == ROWS;
+            const int64_t row_out = parts ? static_cast<int64_t>(it) * PAIR + rbase : T.row0 + rbase;
+            uint16_t* dst = (parts ? p.part_o : p.out) + (row_out + r) * D + hk * 256 + g * 128;
+            uint8_t* seg = smem + P_OFF + (hk * 2 + g) * 8192;
             const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;     // (the same for every row)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -902,7 +912,26 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
                     w[k] = parts ? pack_half2(f[2 * k], f[2 * k + 1]) : *reinterpret_cast<const uint32_t*>(&b2);
                 }
-                if (r < rows) {
+                if (whole) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        *reinterpret_cast<uint4*>(seg + sw128(r, (q & 1) * 4 + k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    if (q & 1) {
+                        fence_async();
+                        bar_sync(5, NSOFT * 32);
+                        if (warp == 0) {
+                            if (elect_one()) {
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    tma_store_2d(parts ? &p_map : &o_map, sbase + P_OFF + z * 8192, z * 128 + (q >> 1) * 64, static_cast<int>(row_out));
+                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                            }
+                            __syncwarp();
+                        }
+                        bar_sync(5, NSOFT * 32);     // the buffers have been read
+                    }
+                } else if (r < rows) {
                     if (wide) {
                         st_global_32(dst + q * 32, w);
                         st_global_32(dst + q * 32 + 16, w + 8);
@@ -914,6 +943,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 }
             }
         }
+        if (warp == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         fence_before();
     }
     __syncwarp();
@@ -957,6 +987,17 @@ static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of 512 16-bit values (the output, the partials) in blocks of 64 rows x 64 dims.
+static bool make_row_map(CUtensorMap* m, uint16_t* rows, int64_t n) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dim[2] = {D, static_cast<cuuint64_t>(n)};
+    const cuuint64_t stride[1] = {D * 2};
+    const cuuint32_t box[2] = {64, ROWS}, ones[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, rows, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace tcp
 
 // Workspace: staged rows (fp16), the new tokens' RoPE table, a flag byte a staged row, the item counter.
@@ -979,14 +1020,17 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
     s.flags = reinterpret_cast<uint8_t*>(s.cs + p.n_rows * 32);
     s.next = reinterpret_cast<int*>(s.flags + ((s.bound + 15) & ~int64_t(15)));
     s.n_items = static_cast<int>(tiles * p.n_splits);
-    CUtensorMap km, vm;
+    CUtensorMap km, vm, om, pm;
+    if (!tcp::make_row_map(&om, p.out, p.n_rows * p.H)) return HCA_ERR_CUDA;
+    pm = om;
+    if (p.n_splits > 1 && !tcp::make_row_map(&pm, p.part_o, tiles * p.n_splits * tcp::PAIR)) return HCA_ERR_CUDA;
     if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF, 2) || !tcp::make_map(&vm, s.rows, s.bound, 32, 4)) return HCA_ERR_CUDA;
     cudaError_t e = cudaFuncSetAttribute(tcp::paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcp::SMEM);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound + (p.inv_freq ? p.n_rows : 0), 8)), 256, 0, st>>>(p, s);
     HCA_CHECK_LAUNCH();
     const int64_t pairs = sm_count() / 2 < s.n_items ? sm_count() / 2 : s.n_items;
-    e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm);
+    e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm, om, pm);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     HCA_CHECK_LAUNCH();
     return HCA_OK;
