@@ -125,7 +125,7 @@ int kv_page_compress(int32_t m, const uint16_t* x, const uint16_t* gate, int64_t
                      void* stream) {
     REQUIRE(n_tokens >= 0 && B >= 0 && max_entries >= 0 && n_slots >= 0);
     if (!layout_ok(layout) || (m != 4 && m != 128)) return HCA_ERR_UNSUPPORTED;
-    if (n_tokens > 0x7FFFFFFFLL || max_entries > 0x7FFFFFFFLL - B) return HCA_ERR_UNSUPPORTED;
+    if (n_tokens > 0x7FFFFFFFLL || max_entries + B > 0x7FFFFFFFLL / 8) return HCA_ERR_UNSUPPORTED;
     if (n_tokens == 0 || B == 0) return HCA_OK;
     REQ_PTR(x); REQ_PTR(gate); REQ_INT(tok_start); REQ_INT(ctx_len); REQ_PTR(pos_bias); REQ_INT(ent_start);
     REQ_PTR(tail_x); REQ_PTR(tail_gate);

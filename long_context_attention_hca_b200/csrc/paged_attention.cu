@@ -614,8 +614,7 @@ static int launch_combine(const Params& p, const Plan& k, cudaStream_t st) {
 template <int D, int R>
 static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
     auto kern = paged_rows_kernel<D, R>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Rows<D, R>::SMEM));
+    const cudaError_t e = allow_smem<paged_rows_kernel<D, R>>(static_cast<int>(Rows<D, R>::SMEM));
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     kern<<<dim3(static_cast<unsigned>(k.tiles), k.splits), 256, Rows<D, R>::SMEM, st>>>(p);
     HCA_CHECK_LAUNCH();

@@ -1025,7 +1025,7 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
     pm = om;
     if (p.n_splits > 1 && !tcp::make_row_map(&pm, p.part_o, tiles * p.n_splits * tcp::PAIR)) return HCA_ERR_CUDA;
     if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF, 2) || !tcp::make_map(&vm, s.rows, s.bound, 32, 4)) return HCA_ERR_CUDA;
-    cudaError_t e = cudaFuncSetAttribute(tcp::paged_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, tcp::SMEM);
+    cudaError_t e = allow_smem<tcp::paged_tc_kernel>(tcp::SMEM);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound + (p.inv_freq ? p.n_rows : 0), 8)), 256, 0, st>>>(p, s);
     HCA_CHECK_LAUNCH();

@@ -234,18 +234,13 @@ page_store_kernel(const uint16_t* __restrict__ x, int64_t n_rows, const int32_t*
     }
 }
 
-// ---------------------------------------------------------------- entry compressor
+// ---------------------------------------------------------------- entry compressors
 // One work item per new entry, and one per request for a step that completes
-// no block of it.  A thread owns 2 channels of the entry (D / 2 threads): few
-// entries complete per step (16K tokens are 120 of m = 128), so the channels
-// have to supply the parallelism, and a thread loads 16 to 32 tokens at a time.
-// The gate is read twice (the block's maximum, then the sums, from L2); the
-// sums run over the tokens in ascending order, as the C ABI fixes them.
-//
-// The tail is read and written in place: the thread that reads a request's
-// tail rows for its first entry is the one that then writes the same channels
-// of the new tail, so no other thread has to be waited for.
-// Bound: DRAM, 4 d bytes a token in.
+// no block of it.  The sums run over the tokens in ascending order, as the C
+// ABI fixes them; the maximum has no order, nor has the computing of the terms.
+// The tail is read and written in place by the same thread (m = 4) or the same
+// CTA with a barrier between (m = 128), channel by channel, so that nothing
+// else has to be waited for.  Bound: DRAM, 4 d bytes a token in.
 struct CompArgs {
     const uint16_t* x;
     const uint16_t* gate;
@@ -271,6 +266,178 @@ __device__ __forceinline__ float2 bf2(uint32_t v) {
     return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
 }
 
+// What an item is: an entry (of request b, tokens e M .. e M + M - 1), or a
+// request whose step completes no block (entry = false).
+struct CompItem {
+    bool entry, tail;           // pool the entry; write the request's new tail (after reading the old one)
+    int b;
+    int64_t e, ctx, q0, end;    // entry; tokens [ctx, end) are the step's, token t at row q0 + t - ctx of x
+};
+
+template <int M>
+__device__ __forceinline__ CompItem comp_item(const CompArgs& a, int64_t it) {
+    CompItem c = {};
+    const int64_t n_ent = min(static_cast<int64_t>(a.ent_start[a.B]), a.max_ent);
+    const bool entry = it < n_ent;
+    c.b = -1;
+    if (entry) c.b = a.ent_req[it];
+    else if (it >= a.max_ent && it < a.max_ent + a.B) c.b = static_cast<int>(it - a.max_ent);
+    if (c.b < 0 || c.b >= a.B) { c.b = -1; return c; }
+    c.ctx = max(a.ctx[c.b], 0);
+    c.q0 = a.tok_start[c.b];
+    c.end = c.ctx + max(min(static_cast<int64_t>(a.tok_start[c.b + 1]), a.n_tok) - c.q0, static_cast<int64_t>(0));
+    if (entry) {
+        c.e = a.ent_pos[it];
+        c.entry = c.e >= c.ctx / M && (c.e + 1) * M <= c.end;
+        c.tail = c.entry && c.e == c.ctx / M;
+    } else {
+        c.tail = c.end > c.ctx && c.ctx / M == c.end / M;       // no block of b completes
+    }
+    return c;
+}
+
+// m = 128: few entries complete per step (16K tokens are 120), so an item is
+// spread over a cluster of d / 64 CTAs of 64 channels each, and inside a CTA
+// over the tokens: warp w takes tokens w, w + 8, ... (16 of them, every load of
+// gate and x in flight at once), the terms e_i and e_i x_i go through shared
+// memory, and one thread per channel adds them up in order.  One thread per two
+// channels for all 128 tokens (the form of m = 4) took 40 us for 16K tokens of d
+// = 512, a round trip to DRAM for every batch of loads.  With RMSNorm the CTAs'
+// sums of squares meet through distributed shared memory, in the C ABI's tree.
+template <int D>
+__global__ void __cluster_dims__(D / 64, 1, 1) __launch_bounds__(256)
+page_compress128_kernel(CompArgs a) {
+    constexpr int M = 128, G = D / 64, TW = M / 8;
+    extern __shared__ float2 terms[];           // [M][64]: e_i, e_i x_i
+    __shared__ float s_max[8][64];
+    __shared__ float s_sum[2], s_all[G];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int grp = blockIdx.x % G;
+    const int64_t it = blockIdx.x / G;
+    const CompItem c = comp_item<M>(a, it);     // the same in every CTA of the cluster
+    if (!c.entry && !c.tail) return;
+    const int ch0 = grp * 64, ch = ch0 + 2 * lane;
+    if (c.entry) {
+        const int64_t t0 = c.e * M;             // token i is in the tail while t0 + i < ctx
+        const size_t toff = static_cast<size_t>(c.b) * M * D + ch;
+        uint32_t gz[TW], xv[TW];
+#pragma unroll
+        for (int j = 0; j < TW; ++j) {
+            const int i = warp + 8 * j;
+            const bool old = t0 + i < c.ctx;
+            const size_t off = old ? toff + static_cast<size_t>(i) * D : static_cast<size_t>(c.q0 + t0 + i - c.ctx) * D + ch;
+            gz[j] = *reinterpret_cast<const uint32_t*>((old ? a.tail_gate : a.gate) + off);
+            xv[j] = *reinterpret_cast<const uint32_t*>((old ? a.tail_x : a.x) + off);
+        }
+        float2 z[TW];
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < TW; ++j) {
+            const float2 bv = __ldg(reinterpret_cast<const float2*>(a.bias + static_cast<size_t>(warp + 8 * j) * D + ch));
+            const float2 gv = bf2(gz[j]);
+            z[j] = make_float2(__fadd_rn(gv.x, bv.x), __fadd_rn(gv.y, bv.y));
+            m0 = fmaxf(m0, z[j].x);
+            m1 = fmaxf(m1, z[j].y);
+        }
+        *reinterpret_cast<float2*>(&s_max[warp][2 * lane]) = make_float2(m0, m1);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            const float2 o = *reinterpret_cast<const float2*>(&s_max[w][2 * lane]);
+            m0 = fmaxf(m0, o.x);
+            m1 = fmaxf(m1, o.y);
+        }
+#pragma unroll
+        for (int j = 0; j < TW; ++j) {
+            const float2 x = bf2(xv[j]);
+            const float e0 = cw_exp_neg(__fsub_rn(z[j].x, m0)), e1 = cw_exp_neg(__fsub_rn(z[j].y, m1));
+            *reinterpret_cast<float4*>(&terms[(warp + 8 * j) * 64 + 2 * lane]) = make_float4(e0, __fmul_rn(e0, x.x), e1, __fmul_rn(e1, x.y));
+        }
+        __syncthreads();                        // (the tail rows have been read, too)
+        float y = 0.0f;
+        if (tid < 64) {
+            float S = 0.0f, N = 0.0f;
+#pragma unroll 16
+            for (int i = 0; i < M; ++i) {
+                const float2 t = terms[i * 64 + tid];
+                S = __fadd_rn(S, t.x);
+                N = __fadd_rn(N, t.y);
+            }
+            y = __fdiv_rn(N, S);
+        }
+        if (a.norm_w) {                         // uniform over the grid
+            if (tid < 64) {
+                float s = __fmul_rn(y, y);
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, o));
+                if (lane == 0) s_sum[warp] = s;
+            }
+            __syncthreads();
+            if (tid < G) {
+                // this CTA's sum into every CTA of the cluster
+                uint32_t at;
+                asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at)
+                             : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(&s_all[grp]))), "r"(tid));
+                asm volatile("st.shared::cluster.f32 [%0], %1;" :: "r"(at), "f"(__fadd_rn(s_sum[0], s_sum[1])) : "memory");
+            }
+            asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+            float s;
+            if constexpr (G == 8)
+                s = __fadd_rn(__fadd_rn(__fadd_rn(s_all[0], s_all[1]), __fadd_rn(s_all[2], s_all[3])),
+                              __fadd_rn(__fadd_rn(s_all[4], s_all[5]), __fadd_rn(s_all[6], s_all[7])));
+            else
+                s = __fadd_rn(s_all[0], s_all[1]);
+            const float r = __fsqrt_rn(__fadd_rn(__fdiv_rn(s, static_cast<float>(D)), a.norm_eps));
+            if (tid < 64) y = __fmul_rn(__fdiv_rn(y, r), __ldg(a.norm_w + ch0 + tid));
+        }
+        // storage: thread = channel; FP8 groups of one warp (g = 32) or both (g = 64), or RoPE dims
+        const int dn = D - a.d_rope, my = ch0 + tid;
+        const int64_t to = a.ent_slot[it];
+        float amax = fabsf(y);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (a.g == 64) {
+            if (tid < 64 && lane == 0) s_max[0][warp] = amax;
+            __syncthreads();
+            amax = fmaxf(s_max[0][0], s_max[0][1]);
+        }
+        if (tid < 64 && to >= 0 && to < a.n_slots) {
+            const float other = __shfl_xor_sync(0xffffffffu, y, 1);      // the pair's other channel
+            if (my < dn) {
+                const float scale = __fdiv_rn(amax, 448.0f);
+                if ((tid & 1) == 0)
+                    *reinterpret_cast<uint16_t*>(a.codes + to * dn + my) =
+                        amax != 0.0f ? f32x2_to_e4m3x2(__fdiv_rn(y, scale), __fdiv_rn(other, scale)) : 0;
+                if (my % a.g == 0) a.scales[to * (dn / a.g) + my / a.g] = scale;
+            } else if ((tid & 1) == 0) {
+                uint32_t w;
+                if (a.inv_freq) {
+                    w = rope_pair_to_bf16(y, other, t0, __ldg(a.inv_freq + (my - dn) / 2));
+                } else {
+                    __nv_bfloat162 h = __floats2bfloat162_rn(y, other);
+                    w = *reinterpret_cast<uint32_t*>(&h);
+                }
+                *reinterpret_cast<uint32_t*>(a.rope + to * a.d_rope + (my - dn)) = w;
+            }
+        }
+    }
+    if (c.tail) {
+        const int64_t t1 = max(c.ctx, c.end / M * M);
+        const int n = static_cast<int>(c.end - t1);              // < M
+        const size_t from = static_cast<size_t>(c.q0 + t1 - c.ctx) * D + ch;
+        const size_t to = (static_cast<size_t>(c.b) * M + static_cast<size_t>(t1 % M)) * D + ch;
+#pragma unroll 8
+        for (int i = warp; i < n; i += 8) {
+            const uint32_t xw = __ldg(reinterpret_cast<const uint32_t*>(a.x + from + static_cast<size_t>(i) * D));
+            const uint32_t gw = __ldg(reinterpret_cast<const uint32_t*>(a.gate + from + static_cast<size_t>(i) * D));
+            *reinterpret_cast<uint32_t*>(a.tail_x + to + static_cast<size_t>(i) * D) = xw;
+            *reinterpret_cast<uint32_t*>(a.tail_gate + to + static_cast<size_t>(i) * D) = gw;
+        }
+    }
+}
+
+// m = 4: many entries, so a thread owns 2 channels of an entry (D / 2 threads),
+// its four tokens' loads in flight at once.
 template <int M, int D>
 __global__ void __launch_bounds__(256)
 page_compress_kernel(CompArgs a) {
@@ -279,69 +446,40 @@ page_compress_kernel(CompArgs a) {
     __shared__ float s_part[8];
     const int ch = (threadIdx.x % TPE) * 2;
     const int64_t it = static_cast<int64_t>(blockIdx.x) * IPB + threadIdx.x / TPE;
-    const int64_t n_ent = min(static_cast<int64_t>(a.ent_start[a.B]), a.max_ent);
+    const CompItem c = comp_item<M>(a, it);
     // every thread of the block stays for the norm's barriers
-    const bool entry = it < n_ent;
-    int b = -1;
-    if (entry) b = a.ent_req[it];
-    else if (it >= a.max_ent && it < a.max_ent + a.B) b = static_cast<int>(it - a.max_ent);
-    const bool any_entry = __syncthreads_or(entry);
-    int64_t ctx = 0, q0 = 0, end = 0;
-    if (b >= 0 && b < a.B) {
-        ctx = max(a.ctx[b], 0);
-        q0 = a.tok_start[b];
-        end = ctx + max(min(static_cast<int64_t>(a.tok_start[b + 1]), a.n_tok) - q0, static_cast<int64_t>(0));
-    } else {
-        b = -1;
-    }
-    bool tail = b >= 0 && end > ctx && !entry && ctx / M == end / M;     // no block of b completes
-    if (any_entry) {
-        const int64_t e = entry ? a.ent_pos[it] : 0;
-        // token e M + i: row i of the tail while it was cached before this step, then row q0 + e M + i - ctx of x
-        const int64_t left = ctx - e * M;
-        const int nt = entry ? static_cast<int>(min(max(left, static_cast<int64_t>(0)), static_cast<int64_t>(M))) : 0;
-        const int64_t xr = q0 + e * M - ctx;
-        const bool ok = entry && b >= 0 && e >= ctx / M && (e + 1) * M <= end;
-        tail = tail || (ok && e == ctx / M);
-        const int64_t toff = static_cast<int64_t>(max(b, 0)) * M * D + ch, xoff = xr * D + ch;
-        const uint16_t *gt = a.tail_gate + toff, *gx = a.gate + xoff, *xt = a.tail_x + toff, *xx = a.x + xoff;
-        auto at = [&](const uint16_t* tl, const uint16_t* xs, int i) -> uint32_t {
-            return ok ? *reinterpret_cast<const uint32_t*>((i < nt ? tl : xs) + i * D) : 0u;
-        };
-        // batches of BT tokens: their loads are all in flight before the first use
-        constexpr int BT = M < 16 ? M : 16;
-        float m0 = -INFINITY, m1 = -INFINITY;
-        const float* bp = a.bias + ch;
-#pragma unroll 1
-        for (int i0 = 0; i0 < M; i0 += 2 * BT) {
-            constexpr int B2 = M < 32 ? M : 2 * BT;
-            uint32_t gz[B2];
+    if (__syncthreads_or(c.entry)) {
+        const int64_t t0 = c.e * M;
+        const size_t toff = static_cast<size_t>(max(c.b, 0)) * M * D + ch;
+        uint32_t gz[M], xv[M];
 #pragma unroll
-            for (int j = 0; j < B2; ++j) gz[j] = at(gt, gx, i0 + j);
-#pragma unroll
-            for (int j = 0; j < B2; ++j) {
-                const float2 gv = bf2(gz[j]), bv = __ldg(reinterpret_cast<const float2*>(bp + (i0 + j) * D));
-                m0 = fmaxf(m0, __fadd_rn(gv.x, bv.x));
-                m1 = fmaxf(m1, __fadd_rn(gv.y, bv.y));
+        for (int i = 0; i < M; ++i) {
+            gz[i] = xv[i] = 0;
+            if (c.entry) {
+                const bool old = t0 + i < c.ctx;
+                const size_t off = old ? toff + static_cast<size_t>(i) * D : static_cast<size_t>(c.q0 + t0 + i - c.ctx) * D + ch;
+                gz[i] = *reinterpret_cast<const uint32_t*>((old ? a.tail_gate : a.gate) + off);
+                xv[i] = *reinterpret_cast<const uint32_t*>((old ? a.tail_x : a.x) + off);
             }
         }
+        float2 z[M];
+        float m0 = -INFINITY, m1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            const float2 gv = bf2(gz[i]), bv = __ldg(reinterpret_cast<const float2*>(a.bias + ch + static_cast<size_t>(i) * D));
+            z[i] = make_float2(__fadd_rn(gv.x, bv.x), __fadd_rn(gv.y, bv.y));
+            m0 = fmaxf(m0, z[i].x);
+            m1 = fmaxf(m1, z[i].y);
+        }
         float S0 = 0.0f, S1 = 0.0f, N0 = 0.0f, N1 = 0.0f;
-#pragma unroll 1
-        for (int i0 = 0; i0 < M; i0 += BT) {
-            uint32_t xv[BT], gz[BT];
 #pragma unroll
-            for (int j = 0; j < BT; ++j) { gz[j] = at(gt, gx, i0 + j); xv[j] = at(xt, xx, i0 + j); }
-#pragma unroll
-            for (int j = 0; j < BT; ++j) {
-                const float2 gv = bf2(gz[j]), bv = __ldg(reinterpret_cast<const float2*>(bp + (i0 + j) * D));
-                const float2 v = bf2(xv[j]);
-                const float e0 = cw_exp_neg(__fsub_rn(__fadd_rn(gv.x, bv.x), m0));
-                const float e1 = cw_exp_neg(__fsub_rn(__fadd_rn(gv.y, bv.y), m1));
-                S0 = __fadd_rn(S0, e0);
-                S1 = __fadd_rn(S1, e1);
-                N0 = __fadd_rn(N0, __fmul_rn(e0, v.x));
-                N1 = __fadd_rn(N1, __fmul_rn(e1, v.y));
-            }
+        for (int i = 0; i < M; ++i) {
+            const float2 v = bf2(xv[i]);
+            const float e0 = cw_exp_neg(__fsub_rn(z[i].x, m0)), e1 = cw_exp_neg(__fsub_rn(z[i].y, m1));
+            S0 = __fadd_rn(S0, e0);
+            S1 = __fadd_rn(S1, e1);
+            N0 = __fadd_rn(N0, __fmul_rn(e0, v.x));
+            N1 = __fadd_rn(N1, __fmul_rn(e1, v.y));
         }
         float y0 = __fdiv_rn(N0, S0), y1 = __fdiv_rn(N1, S1);
         if (a.norm_w) {                     // uniform over the grid
@@ -365,7 +503,7 @@ page_compress_kernel(CompArgs a) {
         const int dn = D - a.d_rope;
         float amax = fmaxf(fabsf(y0), fabsf(y1));
         for (int o = 1; o < a.g / 2; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        const int64_t to = ok ? a.ent_slot[it] : -1;
+        const int64_t to = c.entry ? a.ent_slot[it] : -1;
         if (to >= 0 && to < a.n_slots) {
             if (ch < dn) {
                 const float scale = __fdiv_rn(amax, 448.0f);
@@ -375,7 +513,7 @@ page_compress_kernel(CompArgs a) {
             } else {
                 uint32_t w;
                 if (a.inv_freq) {
-                    w = rope_pair_to_bf16(y0, y1, e * M, __ldg(a.inv_freq + (ch - dn) / 2));
+                    w = rope_pair_to_bf16(y0, y1, t0, __ldg(a.inv_freq + (ch - dn) / 2));
                 } else {
                     __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
                     w = *reinterpret_cast<uint32_t*>(&h);
@@ -384,28 +522,19 @@ page_compress_kernel(CompArgs a) {
             }
         }
     }
-    if (tail) {
-        const int64_t t0 = max(ctx, end / M * M);
-        const size_t toff = (static_cast<size_t>(b) * M) * D + ch;
-        const int n = static_cast<int>(end - t0);            // < M
-        const size_t from = static_cast<size_t>(q0 + t0 - ctx) * D + ch;
-        const size_t to = toff + static_cast<size_t>(t0 % M) * D;
-        constexpr int TB = M < 16 ? M : 16;                  // rows whose loads fly together
-        for (int i0 = 0; i0 < n; i0 += TB) {
-            uint32_t xv[TB], gv[TB];
+    if (c.tail) {
+        const int64_t t1 = max(c.ctx, c.end / M * M);
+        const int n = static_cast<int>(c.end - t1);              // < M
+        const size_t from = static_cast<size_t>(c.q0 + t1 - c.ctx) * D + ch;
+        const size_t to = (static_cast<size_t>(c.b) * M + static_cast<size_t>(t1 % M)) * D + ch;
 #pragma unroll
-            for (int j = 0; j < TB; ++j)
-                if (i0 + j < n) {
-                    xv[j] = *reinterpret_cast<const uint32_t*>(a.x + from + static_cast<size_t>(i0 + j) * D);
-                    gv[j] = *reinterpret_cast<const uint32_t*>(a.gate + from + static_cast<size_t>(i0 + j) * D);
-                }
-#pragma unroll
-            for (int j = 0; j < TB; ++j)
-                if (i0 + j < n) {
-                    *reinterpret_cast<uint32_t*>(a.tail_x + to + static_cast<size_t>(i0 + j) * D) = xv[j];
-                    *reinterpret_cast<uint32_t*>(a.tail_gate + to + static_cast<size_t>(i0 + j) * D) = gv[j];
-                }
-        }
+        for (int i = 0; i < M - 1; ++i)
+            if (i < n) {
+                *reinterpret_cast<uint32_t*>(a.tail_x + to + static_cast<size_t>(i) * D) =
+                    __ldg(reinterpret_cast<const uint32_t*>(a.x + from + static_cast<size_t>(i) * D));
+                *reinterpret_cast<uint32_t*>(a.tail_gate + to + static_cast<size_t>(i) * D) =
+                    __ldg(reinterpret_cast<const uint32_t*>(a.gate + from + static_cast<size_t>(i) * D));
+            }
     }
 }
 
@@ -454,14 +583,17 @@ int page_compress_launch(int m, const uint16_t* x, const uint16_t* gate, int64_t
     CompArgs a = {x, gate, n_tok, tok_start, ctx, B, bias, ent_start, ent_req, ent_pos, ent_slot, max_ent, tail_x,
                   tail_gate, L.d_rope, L.scale_group, pool.codes, pool.scales, pool.rope, n_slots,
                   ex ? ex->norm_w : nullptr, ex ? ex->norm_eps : 0.0f, ex ? ex->inv_freq : nullptr};
-    const int ipb = 256 / (L.d / 2);
-    const unsigned grid = static_cast<unsigned>(ceil_div(max_ent + B, ipb));
-    if (L.d == 512) {
-        if (m == 4) page_compress_kernel<4, 512><<<grid, 256, 0, st>>>(a);
-        else page_compress_kernel<128, 512><<<grid, 256, 0, st>>>(a);
+    const int64_t items = max_ent + B;
+    if (m == 4) {
+        const unsigned grid = static_cast<unsigned>(ceil_div(items, 256 / (L.d / 2)));
+        if (L.d == 512) page_compress_kernel<4, 512><<<grid, 256, 0, st>>>(a);
+        else page_compress_kernel<4, 128><<<grid, 256, 0, st>>>(a);
     } else {
-        if (m == 4) page_compress_kernel<4, 128><<<grid, 256, 0, st>>>(a);
-        else page_compress_kernel<128, 128><<<grid, 256, 0, st>>>(a);
+        constexpr int smem = 128 * 64 * sizeof(float2);
+        auto kern = L.d == 512 ? page_compress128_kernel<512> : page_compress128_kernel<128>;
+        const cudaError_t e = L.d == 512 ? allow_smem<page_compress128_kernel<512>>(smem) : allow_smem<page_compress128_kernel<128>>(smem);
+        if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
+        kern<<<static_cast<unsigned>(items * (L.d / 64)), 256, smem, st>>>(a);
     }
     HCA_CHECK_LAUNCH();
     return HCA_OK;
