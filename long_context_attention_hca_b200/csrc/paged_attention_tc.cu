@@ -78,6 +78,7 @@ struct Stage {
     float2* cs;                 // [n_rows][32]: cos / sin of each new token's RoPE pairs (with inv_freq)
     int* next;                  // the item counter
     int n_items;                // tiles x splits
+    int pairs;                  // CTA pairs of the launch: their first items are 0 .. pairs - 1
 };
 
 // Request b's staged rows start at b per_req + row_start[b]: entries (padded
@@ -99,69 +100,102 @@ __device__ __forceinline__ Region region(const Params& p, const Stage& s, int b,
 }
 
 // ------------------------------------------------------------------ staging
-// A warp per staged row, 16 dims a lane.  Bound: DRAM and L2 (604 or 1024 B in,
-// 1 KB out a row).
+// A warp takes 8 consecutive staged rows: lane l < 8 finds where row l comes
+// from (request, page, pool row), then the warp loads, converts and stores the
+// rows, 16 dims a lane, four rows' loads in flight.  Bound: DRAM and L2 (604 or
+// 1024 B in, 1 KB out a row); one row a warp took 18 us for 33K rows, most of it
+// the chain search -> table -> row of every warp.  Few fat blocks also leave
+// room on the SMs for the attention's CTAs to start beside them.
+constexpr int STAGE_ROWS = 8;                   // a warp
+
 __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
     const int lane = threadIdx.x & 31;
-    const int64_t g = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
     pdl_trigger();                              // the attention's prologue may start
-    if (g == 0 && lane == 0) *s.next = 0;
-    if (g >= s.bound) {
-        // a new token's RoPE table, lane = pair: once here, where every row's conversion and output would go through
+    if (w == 0 && lane == 0) *s.next = s.pairs;
+    const int64_t g0 = w * STAGE_ROWS, stage_warps = (s.bound + STAGE_ROWS - 1) / STAGE_ROWS;
+    if (w >= stage_warps) {
+        // the new tokens' RoPE table, lane = pair: once here, where every row's conversion and output would go through
         // sincos again (7K clocks an item there, most of them instruction fetches)
-        const int64_t n = g - s.bound;
-        if (p.inv_freq == nullptr || n >= p.n_rows || n >= p.row_start[p.B]) return;
-        const int b = last_at_most(p.B, [&](int c) { return p.row_start[c] <= n; });
-        s.cs[n * 32 + lane] = rope_cs(p.inv_freq, lane, (p.ctx[b] > 0 ? p.ctx[b] : 0) + n - p.row_start[b]);
+        const int64_t n0 = (w - stage_warps) * STAGE_ROWS;
+        if (p.inv_freq == nullptr || n0 >= p.n_rows || n0 >= p.row_start[p.B]) return;
+        int b = last_at_most(p.B, [&](int c) { return p.row_start[c] <= n0; });
+        for (int64_t n = n0; n < n0 + STAGE_ROWS && n < p.n_rows && n < p.row_start[p.B]; ++n) {
+            while (b + 1 < p.B && p.row_start[b + 1] <= n) ++b;
+            s.cs[n * 32 + lane] = rope_cs(p.inv_freq, lane, (p.ctx[b] > 0 ? p.ctx[b] : 0) + n - p.row_start[b]);
+        }
         return;
     }
-    const int b = last_at_most(p.B, [&](int c) { return c * s.per_req + p.row_start[c] <= g; });
-    const int64_t st = p.row_start[b];
-    const int64_t en = p.row_start[b + 1] < p.n_rows ? p.row_start[b + 1] : p.n_rows;
-    const int n_new = st < 0 || en < st ? 0 : static_cast<int>(en - st);
-    if (n_new == 0) return;
-    const int64_t ctx = p.ctx[b] > 0 ? p.ctx[b] : 0;
-    const Region r = region(p, s, b, ctx, n_new);
-    int64_t i = g - r.base;
-    if (i < 0) return;
-    uint32_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    int64_t row = -1;
-    const int d0 = lane * 16;
-    if (i < r.n_e64) {
-        if (i < r.n_e) row = entry_row(p, b, static_cast<uint32_t>(i));
-        if (row >= 0) {
-            if (d0 < DN) {
-                const uint4 cv = __ldg(reinterpret_cast<const uint4*>(p.codes + row * DN + d0));
-                dequant16(cv, __ldg(p.scales + row * (DN / 64) + d0 / 64), h);
-            } else {
-                const uint4* rp = reinterpret_cast<const uint4*>(p.rope + row * DR + (d0 - DN));
-                const uint4 a = __ldg(rp), c = __ldg(rp + 1);
-                const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    h[k] = pack_half2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+    // the request of row g0: the largest b with b per_req + row_start[b] <= g0
+    const int b0 = last_at_most(p.B, [&](int c) { return c * s.per_req + p.row_start[c] <= g0; });
+    int64_t from = -1;                          // pool row, -1: a row of zeros
+    int kind = 0;                               // 0: nothing staged here, 1: entry, 2: token
+    const int64_t g = g0 + lane;
+    if (lane < STAGE_ROWS && g < s.bound) {
+        int b = b0;
+        while (b + 1 < p.B && (b + 1) * s.per_req + p.row_start[b + 1] <= g) ++b;
+        const int64_t st = p.row_start[b];
+        const int64_t en = p.row_start[b + 1] < p.n_rows ? p.row_start[b + 1] : p.n_rows;
+        const int n_new = st < 0 || en < st ? 0 : static_cast<int>(en - st);
+        if (n_new > 0) {
+            const int64_t ctx = p.ctx[b] > 0 ? p.ctx[b] : 0;
+            const Region r = region(p, s, b, ctx, n_new);
+            int64_t i = g - r.base;
+            if (i >= 0 && i < r.n_e64) {
+                kind = 1;
+                if (i < r.n_e) from = entry_row(p, b, static_cast<uint32_t>(i));
+            } else if (i >= r.n_e64) {
+                i -= r.n_e64;
+                const int64_t n_t = ctx + n_new - r.w0;
+                if (i < r.f + n_t + HALF) {
+                    kind = 2;
+                    if (i < r.f + n_t) from = token_row(p, b, static_cast<uint32_t>(i < r.f ? i : r.w0 + (i - r.f)));
+                }
             }
         }
-    } else {
-        i -= r.n_e64;
-        const int64_t n_t = ctx + n_new - r.w0;
-        if (i >= r.f + n_t + HALF) return;
-        if (i < r.f + n_t) row = token_row(p, b, static_cast<uint32_t>(i < r.f ? i : r.w0 + (i - r.f)));
-        if (row >= 0) {
-            const uint4* rp = reinterpret_cast<const uint4*>(p.tok + row * D + d0);
-            const uint4 a = __ldg(rp), c = __ldg(rp + 1);
-            const uint32_t w[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+    }
+    const int d0 = lane * 16;
+#pragma unroll 1
+    for (int k0 = 0; k0 < STAGE_ROWS; k0 += 4) {
+        int64_t row[4];
+        int kd[4];
+        uint4 c0[4], c1[4];
+        float sc[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                h[k] = pack_half2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+        for (int k = 0; k < 4; ++k) {
+            row[k] = __shfl_sync(0xffffffffu, from, k0 + k);
+            kd[k] = __shfl_sync(0xffffffffu, kind, k0 + k);
+            c0[k] = c1[k] = make_uint4(0, 0, 0, 0);
+            sc[k] = 0.0f;
+            if (row[k] < 0) continue;
+            if (kd[k] == 1 && d0 < DN) {
+                c0[k] = __ldg(reinterpret_cast<const uint4*>(p.codes + row[k] * DN + d0));
+                sc[k] = __ldg(p.scales + row[k] * (DN / 64) + d0 / 64);
+            } else {
+                const uint4* src = reinterpret_cast<const uint4*>(kd[k] == 1 ? p.rope + row[k] * DR + (d0 - DN) : p.tok + row[k] * D + d0);
+                c0[k] = __ldg(src);
+                c1[k] = __ldg(src + 1);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (kd[k] == 0) continue;
+            uint32_t h[8];
+            if (kd[k] == 1 && d0 < DN) {
+                dequant16(c0[k], sc[k], h);
+            } else {
+                const uint32_t v[8] = {c0[k].x, c0[k].y, c0[k].z, c0[k].w, c1[k].x, c1[k].y, c1[k].z, c1[k].w};
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[i] = pack_half2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
+            }
+            const bool bad = __any_sync(0xffffffffu, any_bad16(h));
+            const uint32_t keep = bad ? 0u : 0xffffffffu;
+            uint4* dst = reinterpret_cast<uint4*>(s.rows + (g0 + k0 + k) * D + d0);
+            dst[0] = make_uint4(h[0] & keep, h[1] & keep, h[2] & keep, h[3] & keep);
+            dst[1] = make_uint4(h[4] & keep, h[5] & keep, h[6] & keep, h[7] & keep);
+            if (lane == 0) s.flags[g0 + k0 + k] = row[k] < 0 ? 1 : (bad ? 2 : 0);
         }
     }
-    const bool bad = __any_sync(0xffffffffu, any_bad16(h));
-    const uint32_t keep = bad ? 0u : 0xffffffffu;
-    uint4* dst = reinterpret_cast<uint4*>(s.rows + g * D + d0);
-    dst[0] = make_uint4(h[0] & keep, h[1] & keep, h[2] & keep, h[3] & keep);
-    dst[1] = make_uint4(h[4] & keep, h[5] & keep, h[6] & keep, h[7] & keep);
-    if (lane == 0) s.flags[g] = row < 0 ? 1 : (bad ? 2 : 0);
 }
 
 // ------------------------------------------------------------------ PTX
@@ -422,7 +456,9 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
     cluster_sync();                                 // barriers and TMEM of both CTAs are ready
     fence_after();
     const uint32_t tmem = c.tmem;
-    pdl_wait();                                     // the staged rows are complete, the counter is zero
+    // From here until a warp's own pdl_wait() the staging kernel may still be running.  It was launched plainly, so that
+    // everything before it is complete: lengths and queries may be read, what it writes (staged rows, flags, RoPE table,
+    // the item counter) not yet.  A pair's first item is its own number; later ones come from the counter.
     bool ok = true;
     const int rbase = rank * ROWS;                  // first row of this CTA in a tile
 
@@ -441,10 +477,13 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const bool leader = elect_one();
         // the next item with rows and keys, posted to both CTAs: where and how much is worked out once, here
         auto post_next = [&](int k, Item& J) {
-            for (;;) {
-                int it = 0;
-                if (lane == 0) it = atomicAdd(s.next, 1);
-                it = __shfl_sync(0xffffffffu, it, 0);
+            for (bool own = k == 0;; own = false) {
+                int it = blockIdx.x >> 1;
+                if (!own) {
+                    if (k == 0) pdl_wait();          // (the counter is set)
+                    if (lane == 0) it = atomicAdd(s.next, 1);
+                    it = __shfl_sync(0xffffffffu, it, 0);
+                }
                 J.index = -1;
                 if (it >= s.n_items) break;
                 if (!make_item(p, s, it, J)) continue;
@@ -481,6 +520,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         Item I, J;
         int u = 0;                                   // key tiles so far: each uses every K slot once
         if (rank == 0) post_next(0, I); else take_item(0, I);
+        pdl_wait();
         for (int k = 0; I.index >= 0 && ok; ++k) {
             for (int i = 0; i < I.n && ok; ++i, ++u) {
                 const int y = static_cast<int>(half_row(I, 2 * (I.k0 + i) + rank));
@@ -494,6 +534,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         if (!ok) for (int i = 0; i < 1000; ++i) __nanosleep(1000);
     } else if (warp == 15) {
         // ------------------------------------------------------------ V copies
+        pdl_wait();
         const bool leader = elect_one();
         Item I;
         int u = 0;
@@ -625,6 +666,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     *reinterpret_cast<uint4*>(my + sw128(w0 + r, ch + 1)) = make_uint4(0, 0, 0, 0);
                 }
             }
+            if (k == 0 && p.inv_freq) pdl_wait();    // (the RoPE table)
             asm volatile("cp.async.wait_all;" ::: "memory");
             // token of a row, counted up: a division per item instead of one per row
             int tok = (T.r0 + rbase + w0) / p.H, head = (T.r0 + rbase + w0) - tok * p.H, cs_tok = tok;
@@ -713,6 +755,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         };
         take_for_all(0);
         bar_sync(5, NSOFT * 32);
+        pdl_wait();                                  // (the flags of the staged rows)
         for (int kk = 0;; ++kk) {
             const Item& I = c.soft_item[kk & 1];     // (read where needed: its fields in registers would spill others)
             const int it = I.index;
@@ -1027,9 +1070,11 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
     if (!tcp::make_map(&km, s.rows, s.bound, tcp::HALF, 2) || !tcp::make_map(&vm, s.rows, s.bound, 32, 4)) return HCA_ERR_CUDA;
     cudaError_t e = allow_smem<tcp::paged_tc_kernel>(tcp::SMEM);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
-    tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(s.bound + (p.inv_freq ? p.n_rows : 0), 8)), 256, 0, st>>>(p, s);
-    HCA_CHECK_LAUNCH();
     const int64_t pairs = sm_count() / 2 < s.n_items ? sm_count() / 2 : s.n_items;
+    s.pairs = static_cast<int>(pairs);
+    const int64_t warps = ceil_div(s.bound, tcp::STAGE_ROWS) + (p.inv_freq ? ceil_div(p.n_rows, tcp::STAGE_ROWS) : 0);
+    tcp::stage_kernel<<<static_cast<unsigned>(ceil_div(warps, 8)), 256, 0, st>>>(p, s);
+    HCA_CHECK_LAUNCH();
     e = launch_pdl(tcp::paged_tc_kernel, dim3(static_cast<unsigned>(2 * pairs)), dim3(tcp::NTHREADS), tcp::SMEM, st, p, s, km, vm, om, pm);
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     HCA_CHECK_LAUNCH();

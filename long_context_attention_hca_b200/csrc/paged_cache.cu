@@ -220,7 +220,7 @@ page_store_kernel(const uint16_t* __restrict__ x, int64_t n_rows, const int32_t*
             __syncwarp();
             if (2 * lane < d_rope) {
                 const float2 ab = *reinterpret_cast<const float2*>(&s_rope[warp][2 * lane]);
-                const uint32_t r = rope_pair_to_bf16(ab.x, ab.y, pos[t], __ldg(inv_freq + lane));
+                const uint32_t r = rotate_to_bf16(ab.x, ab.y, rope_cos_sin(pos[t], __ldg(inv_freq + lane)));
                 *reinterpret_cast<uint32_t*>(pages + static_cast<size_t>(to) * D + dn + 2 * lane) = r;
             }
             if (ch >= dn) return;
@@ -311,6 +311,7 @@ page_compress128_kernel(CompArgs a) {
     extern __shared__ float2 terms[];           // [M][64]: e_i, e_i x_i
     __shared__ float s_max[8][64];
     __shared__ float s_sum[2], s_all[G];
+    __shared__ CosSin s_cs[32];                 // of the entry's position, in the CTA that holds the RoPE dims
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int grp = blockIdx.x % G;
     const int64_t it = blockIdx.x / G;
@@ -355,6 +356,8 @@ page_compress128_kernel(CompArgs a) {
         }
         __syncthreads();                        // (the tail rows have been read, too)
         float y = 0.0f;
+        if (warp == 2 && a.inv_freq && lane < a.d_rope / 2 && grp == G - 1)      // (beside the sums)
+            s_cs[lane] = rope_cos_sin(t0, __ldg(a.inv_freq + lane));
         if (tid < 64) {
             float S = 0.0f, N = 0.0f;
 #pragma unroll 16
@@ -396,11 +399,9 @@ page_compress128_kernel(CompArgs a) {
         float amax = fabsf(y);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        if (a.g == 64) {
-            if (tid < 64 && lane == 0) s_max[0][warp] = amax;
-            __syncthreads();
-            amax = fmaxf(s_max[0][0], s_max[0][1]);
-        }
+        if (tid < 64 && lane == 0) s_max[0][warp] = amax;
+        __syncthreads();
+        if (a.g == 64) amax = fmaxf(s_max[0][0], s_max[0][1]);
         if (tid < 64 && to >= 0 && to < a.n_slots) {
             const float other = __shfl_xor_sync(0xffffffffu, y, 1);      // the pair's other channel
             if (my < dn) {
@@ -412,7 +413,7 @@ page_compress128_kernel(CompArgs a) {
             } else if ((tid & 1) == 0) {
                 uint32_t w;
                 if (a.inv_freq) {
-                    w = rope_pair_to_bf16(y, other, t0, __ldg(a.inv_freq + (my - dn) / 2));
+                    w = rotate_to_bf16(y, other, s_cs[(my - dn) / 2]);
                 } else {
                     __nv_bfloat162 h = __floats2bfloat162_rn(y, other);
                     w = *reinterpret_cast<uint32_t*>(&h);
@@ -513,7 +514,7 @@ page_compress_kernel(CompArgs a) {
             } else {
                 uint32_t w;
                 if (a.inv_freq) {
-                    w = rope_pair_to_bf16(y0, y1, t0, __ldg(a.inv_freq + (ch - dn) / 2));
+                    w = rotate_to_bf16(y0, y1, rope_cos_sin(t0, __ldg(a.inv_freq + (ch - dn) / 2)));
                 } else {
                     __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
                     w = *reinterpret_cast<uint32_t*>(&h);
