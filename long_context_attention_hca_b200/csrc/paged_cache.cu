@@ -166,12 +166,15 @@ page_store_kernel(const uint16_t* __restrict__ x, int64_t n_rows, const int32_t*
     __shared__ float s_rope[8][64];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * 8 + warp;
-    if (t >= n_rows || t >= *n_live) return;
+    if (t >= n_rows) return;
+    // everything the token needs is asked for at once; whether it is to be stored is known later
+    const int live = *n_live;
     const int64_t to = slot[t];
-    if (to < 0 || to >= n_slots) return;
     const int ch = lane * C;
     const uint16_t* src = x + static_cast<size_t>(t) * D + ch;
-    uint16_t* dst = pages + static_cast<size_t>(to) * D + ch;
+    const bool pair = inv_freq && 2 * lane < d_rope;
+    const int32_t at = inv_freq ? pos[t] : 0;
+    const float fr = pair ? __ldg(inv_freq + lane) : 0.0f;
     uint32_t w[C / 2];
     if constexpr (C >= 8) {
 #pragma unroll
@@ -179,7 +182,11 @@ page_store_kernel(const uint16_t* __restrict__ x, int64_t n_rows, const int32_t*
     } else {
         *reinterpret_cast<uint2*>(w) = __ldg(reinterpret_cast<const uint2*>(src));
     }
+    if (t >= live || to < 0 || to >= n_slots) return;
+    uint16_t* dst = pages + static_cast<size_t>(to) * D + ch;
     if (norm_w || inv_freq) {
+        CosSin cs = {1.0, 0.0};
+        if (pair) cs = rope_cos_sin(at, fr);
         float y[C];
 #pragma unroll
         for (int i = 0; i < C / 2; ++i) {
@@ -218,9 +225,9 @@ page_store_kernel(const uint16_t* __restrict__ x, int64_t n_rows, const int32_t*
 #pragma unroll
                 for (int i = 0; i < C; ++i) s_rope[warp][ch - dn + i] = y[i];
             __syncwarp();
-            if (2 * lane < d_rope) {
+            if (pair) {
                 const float2 ab = *reinterpret_cast<const float2*>(&s_rope[warp][2 * lane]);
-                const uint32_t r = rotate_to_bf16(ab.x, ab.y, rope_cos_sin(pos[t], __ldg(inv_freq + lane)));
+                const uint32_t r = rotate_to_bf16(ab.x, ab.y, cs);
                 *reinterpret_cast<uint32_t*>(pages + static_cast<size_t>(to) * D + dn + 2 * lane) = r;
             }
             if (ch >= dn) return;
