@@ -912,15 +912,15 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             const float2* row_cs = s.cs + (I.tok_row + tok) * 32;
             if (rot && one_tok) cs = row_cs[lane];
             bar_sync(5, NSOFT * 32);                 // c.mx is read: the next item may write it
-            // O: row r, dims 256 hk + 128 g .. + 127, half of them at a time.  64 rows (always, with 64 heads; partials
-            // always): through the P buffers (free now) as four blocks of 64 rows x 64 dims, 128-byte swizzle, each
-            // stored by one TMA copy.  Fewer rows: straight from registers, 32 bytes (a sector) a store where the output
-            // allows it (for all rows, that kept the load/store unit busy for 4K clocks an item, and the next item's
-            // query conversion waiting).
+            // O: row r, dims 256 hk + 128 g .. + 127, 32 of them at a time.  64 rows (always, with 64 heads; partials
+            // always): through the P buffers (free now) in turn, four blocks of 64 rows x 32 dims (64-byte swizzle) each
+            // stored by one TMA copy while the next 32 dims are read and rounded.  Fewer rows: straight from registers,
+            // 32 bytes (a sector) a store where the output allows it (for all rows, that kept the load/store unit busy
+            // for 4K clocks an item, and the next item's query conversion waiting).
             const bool whole = parts || rows == ROWS;
             const int64_t row_out = parts ? static_cast<int64_t>(it) * PAIR + rbase : T.row0 + rbase;
             uint16_t* dst = (parts ? p.part_o : p.out) + (row_out + r) * D + hk * 256 + g * 128;
-            uint8_t* seg = smem + P_OFF + (hk * 2 + g) * 8192;
+            uint8_t* seg = smem + P_OFF + (hk * 2 + g) * 4096 + r * 64;
             const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;     // (the same for every row)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -956,24 +956,26 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     w[k] = parts ? pack_half2(f[2 * k], f[2 * k + 1]) : *reinterpret_cast<const uint32_t*>(&b2);
                 }
                 if (whole) {
+                    if (q > 0) bar_sync(5, NSOFT * 32);      // this round's buffer has been read
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        *reinterpret_cast<uint4*>(seg + sw128(r, (q & 1) * 4 + k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-                    if (q & 1) {
-                        fence_async();
-                        bar_sync(5, NSOFT * 32);
-                        if (warp == 0) {
-                            if (elect_one()) {
+                        *reinterpret_cast<uint4*>(seg + (q & 1) * 16384 + ((k ^ ((r >> 1) & 3)) << 4)) =
+                            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+                    fence_async();
+                    bar_sync(5, NSOFT * 32);
+                    if (warp == 0) {
+                        if (elect_one()) {
 #pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    tma_store_2d(parts ? &p_map : &o_map, sbase + P_OFF + z * 8192, z * 128 + (q >> 1) * 64, static_cast<int>(row_out));
-                                asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                                asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                            }
-                            __syncwarp();
+                            for (int z = 0; z < 4; ++z)
+                                tma_store_2d(parts ? &p_map : &o_map, sbase + P_OFF + (q & 1) * 16384 + z * 4096, z * 128 + q * 32,
+                                             static_cast<int>(row_out));
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                            if (q < 3) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                            else asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                         }
-                        bar_sync(5, NSOFT * 32);     // the buffers have been read
+                        __syncwarp();
                     }
+                    if (q == 3) bar_sync(5, NSOFT * 32);     // P may be written again
                 } else if (r < rows) {
                     if (wide) {
                         st_global_32(dst + q * 32, w);
@@ -1030,15 +1032,15 @@ static bool make_map(CUtensorMap* m, uint16_t* rows, int64_t bound, uint32_t box
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows of 512 16-bit values (the output, the partials) in blocks of 64 rows x 64 dims.
+// Rows of 512 16-bit values (the output, the partials) in blocks of 64 rows x 32 dims.
 static bool make_row_map(CUtensorMap* m, uint16_t* rows, int64_t n) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t dim[2] = {D, static_cast<cuuint64_t>(n)};
     const cuuint64_t stride[1] = {D * 2};
-    const cuuint32_t box[2] = {64, ROWS}, ones[2] = {1, 1};
+    const cuuint32_t box[2] = {32, ROWS}, ones[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, rows, dim, stride, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace tcp
