@@ -741,8 +741,6 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         const int hk = qd >> 1;                      // which half of the tile's keys
         const int r = (qd & 1) * 32 + lane;          // row of this CTA
         const uint32_t lb = tmem + (static_cast<uint32_t>(qd * 32) << 16);
-        const uint32_t p_first = in_first(smem_u32(&c.p_full[g])), s_first = in_first(smem_u32(&c.s_free[g]));
-        const uint32_t o_first = in_first(smem_u32(&c.o_free));
         int uses[2] = {0, 0};                        // of each parity's buffers, so far
         // one warp takes an item for all eight (they meet at barriers: all go on, or none), the next one ahead of the
         // output of this one: the fence in there would wait for the output's stores
@@ -761,21 +759,16 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             const int it = I.index;
             if (it < 0) break;
             const Tile& T = I.T;
-            const int n = I.n;
-            const int rows = min(max(T.rows - rbase, 0), ROWS);
-            const int rt = min(rbase + r, T.rows - 1);
-            const int tok = (T.r0 + rt) / p.H;
-            const RowKeys rk = row_keys(p, T, T.ctx + tok);
-            const int w0s = T.n_e + T.n_f;           // first window slot
+            const RowKeys rk = row_keys(p, T, T.ctx + (T.r0 + min(rbase + r, T.rows - 1)) / p.H);
             float m_l = -INFINITY, l_run = 0.0f;     // this thread's share of l, and the maximum it is relative to
             uint32_t fl[2];
             auto flags_of = [&](int i) {
-                const uint8_t* f = s.flags + (i < n ? half_row(I, 2 * (I.k0 + i) + hk) : I.ent0) + lane;
+                const uint8_t* f = s.flags + (i < I.n ? half_row(I, 2 * (I.k0 + i) + hk) : I.ent0) + lane;
                 fl[0] = f[0];
                 fl[1] = f[32];
             };
             flags_of(g);
-            for (int i = g; i < n; i += 2) {
+            for (int i = g; i < I.n; i += 2) {
                 const int h = 2 * (I.k0 + i) + hk, use = uses[g] + (i >> 1);
                 if (ok) ok = wait_bar(smem_u32(&c.s_full[g]), use & 1, abort_flag);
                 fence_after();
@@ -791,7 +784,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 }
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(s_first);            // S may be overwritten
+                if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.s_free[g])));            // S may be overwritten
                 // keys that this row sees among the half tile's 64, as bits
                 auto below = [](int k) -> unsigned { return k <= 0 ? 0u : (k >= 32 ? 0xffffffffu : (1u << k) - 1u); };
                 unsigned vis[2], bad = 0;
@@ -803,7 +796,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     } else if (h < I.h_e + I.h_f) {
                         vis[z] = below(T.n_f - ((h - I.h_e) * HALF + z * 32));
                     } else {
-                        const int k0 = w0s + (h - I.h_e - I.h_f) * HALF + z * 32;     // slot of the first of these keys
+                        const int k0 = T.n_e + T.n_f + (h - I.h_e - I.h_f) * HALF + z * 32;   // slot of the first of these keys
                         vis[z] = h < I.n_half ? below(rk.w_hi + 1 - k0) & (~below(rk.w_from - k0) | below(rk.f_to - k0)) : 0u;
                     }
                     vis[z] &= ~gone;
@@ -837,7 +830,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                     m_new = m_tile;
                 }
                 if (hk == 0) c.m[i & 1][r] = m_new;
-                if (i + 1 < n) asm volatile("bar.arrive %0, 256;" :: "r"(3 + ((i + 1) & 1)) : "memory");
+                if (i + 1 < I.n) asm volatile("bar.arrive %0, 256;" :: "r"(3 + ((i + 1) & 1)) : "memory");
                 const float ref = m_new == -INFINITY ? 0.0f : m_new;
                 uint32_t pk[32];
                 // l sums the probabilities in fp32 as they are; PV uses them rounded to fp16, which weighs a key by at
@@ -882,17 +875,20 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 fence_async();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(p_first);
+                if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.p_full[g])));
             }
             take_for_all(kk + 1);
+            const int rows = min(max(T.rows - rbase, 0), ROWS);
+            const int rt = min(rbase + r, T.rows - 1);
+            const int tok = (T.r0 + rt) / p.H;
             // ---- the item's output.  The last tile's group waits for the last PV (it has seen the phase before; the
             // other group may not have)
-            if (g == ((n - 1) & 1) && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (uses[g] + ((n - 1) >> 1)) & 1, abort_flag);
-            uses[0] += (n + 1) / 2;
-            uses[1] += n / 2;
+            if (g == ((I.n - 1) & 1) && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (uses[g] + ((I.n - 1) >> 1)) & 1, abort_flag);
+            uses[0] += (I.n + 1) / 2;
+            uses[1] += I.n / 2;
             bar_sync(5, NSOFT * 32);
             fence_after();
-            const float m_used = c.m[(n - 1) & 1][r];
+            const float m_used = c.m[(I.n - 1) & 1][r];
             c.mx[g][hk][r] = m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_used);
             bar_sync(5, NSOFT * 32);
             float l = c.mx[0][0][r] + c.mx[0][1][r] + c.mx[1][0][r] + c.mx[1][1][r];
@@ -924,36 +920,31 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;     // (the same for every row)
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
-                uint32_t o[32];
-                tmem_ld32(lb + O_COL + g * 128 + q * 32, o);
+                uint32_t w[32];                      // O, then its rounded pairs in the first half
+                tmem_ld32(lb + O_COL + g * 128 + q * 32, w);
                 tmem_wait_ld();
                 if (q == 3) {                        // O has been read
                     fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(o_first);
+                    if (lane == 0) mbar_arrive_cluster(in_first(smem_u32(&c.o_free)));
                 }
-                float f[32];
+                const bool turn = rot && q >= 2;
 #pragma unroll
-                for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(o[j]) * inv;
-                if (rot && q >= 2) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
+                for (int j = 0; j < 16; ++j) {
+                    float x = __uint_as_float(w[2 * j]) * inv, y = __uint_as_float(w[2 * j + 1]) * inv;
+                    if (turn) {
                         float zx = __shfl_sync(0xffffffffu, cs.x, (q & 1) * 16 + j), zy = __shfl_sync(0xffffffffu, cs.y, (q & 1) * 16 + j);
                         if (!one_tok) {              // few heads: the neighbours are other tokens' rows
                             const float2 z = row_cs[(q & 1) * 16 + j];
                             zx = z.x;
                             zy = z.y;
                         }
-                        const float x = f[2 * j], y = f[2 * j + 1];
-                        f[2 * j] = x * zx + y * zy;
-                        f[2 * j + 1] = y * zx - x * zy;
+                        const float x2 = x * zx + y * zy;
+                        y = y * zx - x * zy;
+                        x = x2;
                     }
-                }
-                uint32_t w[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(f[2 * k], f[2 * k + 1]);
-                    w[k] = parts ? pack_half2(f[2 * k], f[2 * k + 1]) : *reinterpret_cast<const uint32_t*>(&b2);
+                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+                    w[j] = parts ? pack_half2(x, y) : *reinterpret_cast<const uint32_t*>(&b2);
                 }
                 if (whole) {
                     if (q > 0) bar_sync(5, NSOFT * 32);      // this round's buffer has been read
