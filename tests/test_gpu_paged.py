@@ -78,7 +78,7 @@ def plan_ref(ctx, new, m, P, table, free, n_free):
 
 @pytest.mark.parametrize("B,m,P,maxc,maxn,short", [
     (1, 1, 1, 0, 1, 0), (1, 1, 64, 1000, 1, 0), (5, 1, 16, 300, 40, 0), (33, 128, 16, 70000, 1500, 0),
-    (700, 1, 48, 500, 90, 0), (1500, 4, 64, 3000, 64, 0), (9, 1, 16, 200, 100, 7), (40, 4, 8, 900, 400, 1000)])
+    (700, 1, 48, 500, 90, 0), (1500, 4, 64, 3000, 64, 0), (16384, 1, 64, 40, 2, 0), (9, 1, 16, 200, 100, 7), (40, 4, 8, 900, 400, 1000)])
 def test_plan(B, m, P, maxc, maxn, short):
     r = np.random.default_rng(B * 7 + m)
     ctx = r.integers(0, maxc + 1, B)
@@ -217,6 +217,42 @@ def test_compress_bits_over_ragged_steps(d, m, extras, P):
     for b in range(B):
         untouched[pool.rows(b, int(ctx[b]) // m)] = False
     assert not host(cache.codes).reshape(-1, dn)[untouched].any()
+
+
+def test_plan_accepts_slices_and_repeats():
+    """Integer arrays may be slices of longer ones; the same call twice gives the same plan (nothing is consumed)."""
+    big = torch.arange(100, dtype=torch.int32, device=DEV)
+    lens = i32([9, 7, 20, 1, 30])
+    t = torch.full((3, 9), -1, dtype=torch.int32, device=DEV)
+    t[0, :2], t[1, :3] = i32([91, 92]), i32([93, 94, 95])
+    a = hca.kv_page_plan(lens[1:4], lens[:3], 1, 4, t, big[7:50], big[37:38], max_rows=40)
+    first = (t.clone(), a.slot.clone(), a.free_left.clone())
+    b = hca.kv_page_plan(lens[1:4], lens[:3], 1, 4, t, big[7:50], big[37:38], max_rows=40)
+    assert torch.equal(t, first[0]) and torch.equal(b.slot, first[1]) and torch.equal(b.free_left, first[2])
+    assert a.row_start.tolist() == [0, 9, 16, 36] and a.slot[:3].tolist() == [92 * 4 + 3, 43 * 4, 43 * 4 + 1]
+
+
+@pytest.mark.parametrize("m", [4, 128])
+def test_compress_without_a_page(m):
+    """Entries that got no page are not stored, the others are, and the tails move on all the same."""
+    d, B = 128, 3
+    g = gen(m)
+    new = [2 * m + 3, m + 1, m - 1]
+    x, gate = bf((sum(new), d), g), bf((sum(new), d), g)
+    bias = torch.randn((m, d), generator=g, device=DEV) * 0.5
+    table = torch.full((B, 4), -1, dtype=torch.int32, device=DEV)
+    ctx, nl = i32([0] * B), i32(new)
+    plan = hca.kv_page_plan(ctx, nl, m, 1, table, i32([5, 2]), i32([2]), max_rows=6)
+    assert plan.missing.tolist() == [1] and plan.slot.tolist() == [2, 5, -1, -1, -1, -1]
+    cache = hca.KVCache(8, 1, LAYOUTS[d], zero=True)
+    tx, tg = torch.zeros((B, m, d), dtype=torch.bfloat16, device=DEV), torch.zeros((B, m, d), dtype=torch.bfloat16, device=DEV)
+    starts = i32(np.concatenate([[0], np.cumsum(new)]))
+    hca.kv_page_compress(x, gate, bias, starts, ctx, plan, tx, tg, cache)
+    ref = oracle.compress(host(x[None, :2 * m]), host(gate[None, :2 * m]), host(bias), m, 2, 32, 32)[0]
+    codes = host(cache.codes).reshape(8, -1)
+    assert np.array_equal(codes[[2, 5]], ref[0])
+    assert not np.delete(codes, [2, 5], 0).any()
+    assert torch.equal(tx[0, :3], x[2 * m:2 * m + 3]) and torch.equal(tx[1, 0], x[2 * m + 3 + m]) and torch.equal(tx[2, :m - 1], x[-(m - 1):])
 
 
 # ------------------------------------------------------------------ attention
@@ -388,6 +424,69 @@ def test_attention_many_splits_and_long_offsets():
     """One decode request over 20000 entries (every SM takes a split), pages far into a large pool."""
     c = Case(512, 64, [20000 * 4 - 1], [1], 128, m=4, PE=64, PT=64)
     c.check(c.run(max_new=1))
+
+
+@pytest.mark.parametrize("k", [0, 6, 8])
+def test_tables_too_wide_to_stage(k):
+    """Tables whose entries would take more workspace than is staged: the row kernel serves d = 512 as well."""
+    c = Case(seed=k, **{**CASES[k], "m": CASES[k].get("m") or 4, "n_first": 0})
+    wide = torch.full((len(c.ctx), (3 << 20) // c.PE), -1, dtype=torch.int32, device=DEV)
+    wide[:, :c.ew] = c.etab
+    narrow, c.etab = c.etab, wide
+    got = c.run(max_new=max(c.new))
+    assert hca.paged_attn_workspace_size(c.q.shape[0], len(c.ctx), c.H, c.layout, max(c.new), wide.shape[1] * c.PE, c.W) < 1 << 29
+    c.etab = narrow
+    c.check(got)
+
+
+def test_no_new_tokens_and_padded_rows():
+    """Requests without new tokens only, and a padded batch: nothing but the live rows is written."""
+    for d, H in ((512, 64), (128, 8)):
+        c = Case(d, H, [300, 20, 5], [2, 0, 3], 64, m=4, pad=200)
+        want = c.run()
+        out = torch.full_like(c.q, 7.0)
+        got = c.run(out=out)
+        assert torch.equal(got[:5], want[:5]) and torch.all(got[5:] == 7.0)
+        c.starts, c.lens = np.zeros(4, np.int64), None
+        assert torch.all(c.run(out=torch.full_like(c.q, 7.0)) == 7.0)
+
+
+def test_outputs_on_a_16_byte_boundary():
+    """out, q and ws need 16-byte alignment only (no wider store is assumed)."""
+    for kw in (CASES[4], CASES[8], CASES[1]):
+        c = Case(seed=3, **kw)
+        want = c.run()
+        n = c.q.numel()
+        flat = torch.zeros(n + 8, dtype=torch.bfloat16, device=DEV)
+        q = torch.empty(n + 8, dtype=torch.bfloat16, device=DEV)[8:].view_as(c.q)
+        q.copy_(c.q)
+        need = hca.paged_attn_workspace_size(c.q.shape[0], len(c.ctx), c.H, c.layout, 0, c.ew * c.PE if c.m else 0, c.W, c.n_first)
+        ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)[16:]
+        got = c.run(q=q, out=flat[8:].view_as(c.q), ws=ws)
+        assert torch.equal(got[:c.N], want[:c.N]) and torch.all(flat[:8] == 0)
+
+
+def test_a_query_that_is_not_finite_stays_alone():
+    for d, H in ((512, 64), (128, 8)):
+        c = Case(d, H, [500, 40], [6, 3], 64, m=4)
+        clean = c.run()
+        c.q[2, 1, 7] = float("inf")
+        c.q[4, 3, 0] = float("nan")
+        got = c.run()
+        assert torch.isnan(got[2, 1]).all() and torch.isnan(got[4, 3]).all()
+        keep = torch.ones((9, H), dtype=torch.bool, device=DEV)
+        keep[2, 1] = keep[4, 3] = False
+        assert torch.equal(got[:9][keep], clean[:9][keep])
+
+
+def test_many_requests_of_mixed_lengths():
+    """More requests than a search round has lanes, most without new tokens; sampled rows against the oracle."""
+    r = np.random.default_rng(5)
+    for d, H in ((512, 64), (128, 8)):
+        ctx = r.integers(0, 700, 130).tolist()
+        new = np.where(r.random(130) < 0.6, 0, r.integers(1, 9, 130)).tolist()
+        c = Case(d, H, ctx, new, 40, m=4, PE=8, PT=8, extras=True)
+        c.check(c.run(max_new=8), rows=set(r.integers(0, c.N, 25).tolist()))
 
 
 def test_token_rows_beyond_32_bits():
