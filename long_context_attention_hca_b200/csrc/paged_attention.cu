@@ -86,7 +86,7 @@ __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(256, 1) paged_rows_kernel(Params p) {
+__global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Params p) {
     using C = Rows<D, R>;
     extern __shared__ __align__(128) char smem[];
     char* qs = smem;
@@ -565,14 +565,18 @@ inline int tile_rows(int64_t max_new, int H) { return max_new * H <= 16 ? 16 : 6
 inline int64_t tile_count(int64_t n_rows, int H, int B, int R) { return n_rows * H / R + B; }
 
 // Splits: enough work for every SM (pair) when the tiles alone are too few, but
-// at least min_tiles key tiles for each (max_keys: the longest key list there
-// can be).
-inline int split_count(int64_t slots, int64_t tiles, int64_t max_keys, int tile_keys, int min_tiles) {
+// at least two key tiles for each (max_keys: the longest key list there can be)
+// and only where that shortens a tile's chain by more than the combine costs
+// (join, in key tiles: a pair takes 1.15 us a tile and the combine 6 us; 32
+// requests of 6 tiles took 44 us in two splits and 30 us whole, 4 requests of 65
+// tiles take 36 us in 18 splits where one pair's 65 tiles alone would be 75).
+inline int split_count(int64_t slots, int64_t tiles, int64_t max_keys, int tile_keys, int join) {
+    const int64_t keys = ceil_div(max_keys, tile_keys);
     int64_t s = slots / (tiles > 0 ? tiles : 1);
-    const int64_t by_len = ceil_div(ceil_div(max_keys, tile_keys), min_tiles);
-    if (s > by_len) s = by_len;
+    if (s > ceil_div(keys, 2)) s = ceil_div(keys, 2);
     if (s > MAX_SPLITS) s = MAX_SPLITS;
-    return s < 1 ? 1 : static_cast<int>(s);
+    if (s <= 1 || keys - ceil_div(keys, s) <= join) return 1;
+    return static_cast<int>(s);
 }
 
 struct Plan { bool pairs; int R, splits; int64_t tiles; size_t stage_bytes; };
@@ -590,7 +594,7 @@ static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int6
     const int64_t busy = max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs;
     if (k.pairs) {
         k.stage_bytes = tc_stage_bytes(stage_rows, n_rows);
-        k.splits = split_count(sm_count() / 2, busy, max_keys, 128, 2);
+        k.splits = split_count(sm_count() / 2, busy, max_keys, 128, 5);
     } else {
         k.splits = split_count(sm_count(), busy, max_keys, TK, 2);
     }

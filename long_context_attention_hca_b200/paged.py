@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -219,9 +220,16 @@ def kv_page_compress(x, gate, pos_bias, row_start, ctx_len, plan: PagePlan, tail
 
 
 def paged_attn_workspace_size(n_rows, B, H, layout, max_new, max_entries, W, n_first=0) -> int:
-    """Bytes of ws for paged_attn_chunk (max_entries = entry table width x page
-    size, n_first = 0) and paged_attn_window (max_entries = 0)."""
+    """Bytes of ws on the current device for paged_attn_chunk (max_entries =
+    entry table width x page size, n_first = 0) and paged_attn_window
+    (max_entries = 0)."""
     return int(_lib.paged_attn_workspace_size(n_rows, B, H, _layout(layout), max_new or 0, max_entries, W, n_first))
+
+
+@functools.lru_cache(maxsize=256)
+def _ws_bytes(dev, N, B, H, layout, max_new, max_entries, W, n_first):
+    with _on(dev):
+        return int(_lib.paged_attn_workspace_size(N, B, H, _layout(layout), max_new, max_entries, W, n_first))
 
 
 def _attn_extras(extras, H, layout, dev):
@@ -260,7 +268,7 @@ def _attn(q, row_start, ctx_len, pages, token_table, W, scale, m, cache, entry_t
     lay = _LAYOUT[layout]
     ex = _attn_extras(extras, H, layout, dev)
     with _on(dev):
-        need = _lib.paged_attn_workspace_size(N, B, H, lay, max_new, max_entries, W, n_first)
+        need = _ws_bytes(dev, N, B, H, layout, max_new, max_entries, W, n_first)
         # what is allocated here belongs to the stream that writes it
         if stream is None:
             if out is None:
