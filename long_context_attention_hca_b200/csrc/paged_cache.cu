@@ -27,6 +27,7 @@ namespace {
 // table columns that this step does not write, and the free count left is a
 // separate output.
 constexpr int kPlanThreads = 512;
+constexpr int kPlanMaxB = 16384;            // the C ABI's bound
 
 struct PlanArgs {
     const int32_t* ctx;
@@ -324,6 +325,9 @@ page_compress128_kernel(CompArgs a) {
     const int64_t it = blockIdx.x / G;
     const CompItem c = comp_item<M>(a, it);     // the same in every CTA of the cluster
     if (!c.entry && !c.tail) return;
+    // a CTA's shared memory may be written by another once it is known to have started; waited for where that is
+    const bool meet = c.entry && a.norm_w;
+    if (meet) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int ch0 = grp * 64, ch = ch0 + 2 * lane;
     if (c.entry) {
         const int64_t t0 = c.e * M;             // token i is in the tail while t0 + i < ctx
@@ -375,7 +379,8 @@ page_compress128_kernel(CompArgs a) {
             }
             y = __fdiv_rn(N, S);
         }
-        if (a.norm_w) {                         // uniform over the grid
+        if (meet) {                             // uniform over the cluster
+            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
             if (tid < 64) {
                 float s = __fmul_rn(y, y);
 #pragma unroll
@@ -556,8 +561,8 @@ int page_plan_launch(const int32_t* ctx, const int32_t* nnew, int B, int m, int 
                   row_start, row_req, row_pos, slot, missing, free_left};
     const size_t smem = 2 * (static_cast<size_t>(B) + 1) * sizeof(int32_t);
     if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
+        // (the largest B's, so that two threads' calls cannot lower it under each other's launch)
+        const cudaError_t e = allow_smem<page_plan_kernel>(2 * (kPlanMaxB + 1) * static_cast<int>(sizeof(int32_t)));
         if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     }
     // a thread per row until every SM has a CTA; beyond that a CTA's scan costs more than further rows
