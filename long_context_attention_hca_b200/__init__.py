@@ -290,8 +290,10 @@ class KVCache:
         for t, dt, n in ((codes, torch.uint8, "codes"), (scales, torch.float32, "scales"),
                          (rope, torch.bfloat16, "rope")):
             _need(t, dt, n)
-        if codes.dim() != 3 or not (codes.shape[:2] == scales.shape[:2] == rope.shape[:2]):
+        if not (codes.dim() == scales.dim() == rope.dim() == 3 and codes.shape[:2] == scales.shape[:2] == rope.shape[:2]):
             raise ValueError("codes, scales, rope: [B][capacity][...] of the same B and capacity")
+        if not (codes.device == scales.device == rope.device):
+            raise ValueError("codes, scales, rope: must be on one device")
         dn, dr = codes.shape[2], rope.shape[2]
         layout = {(448, 64): LAYOUT_512, (96, 32): LAYOUT_128}.get((dn, dr))
         if layout is None or scales.shape[2] != dn // layout[2]:

@@ -685,7 +685,7 @@ class PagedLoop:
         self.n_free_tokens.copy_(tp.free_left)
         self.n_free_entries.copy_(ep.free_left)
         self.short.add_(tp.missing).add_(ep.missing)
-        self.ctx.add_(new_len)
+        self.ctx.add_(new_len.clamp(min=0))            # (a length below zero counts as zero, as in the plans)
         return outs
 
     def missing(self) -> int:

@@ -121,6 +121,42 @@ def test_plan_fewer_rows_than_items_negative_lengths_and_no_requests():
     assert none.row_start.tolist() == [0] and none.free_left.tolist() == [2] and none.slot.tolist() == [-1] * 3
 
 
+def test_plans_of_many_requests_from_two_threads():
+    """Beyond 6000 requests a plan asks for more shared memory than a launch has
+    by itself: calls of different B at once, each with the same answer as alone."""
+    import threading
+    jobs, errors = [], []
+    for B in (16384, 6500):
+        ctx, new = i32(np.arange(B) % 50), i32(np.arange(B) % 3)
+        plan = lambda n=3 * B: hca.PagePlan.empty(B, n)
+        table = torch.full((B, 1), -1, dtype=torch.int32, device=DEV)
+        jobs.append((ctx, new, table, i32(np.arange(B)), i32([B]), plan(), plan(), torch.cuda.Stream()))
+    for ctx, new, table, free, count, want, _, _ in jobs:
+        hca.kv_page_plan(ctx, new, 1, 64, table, free, count, plan=want)
+    torch.cuda.synchronize()
+    for job in jobs:
+        job[2].fill_(-1)
+    torch.cuda.synchronize()
+
+    def work(ctx, new, table, free, count, want, got, stream):
+        try:
+            for _ in range(200):
+                hca.kv_page_plan(ctx, new, 1, 64, table, free, count, plan=got, stream=stream)
+        except Exception as e:                          # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for *_, want, got, _ in jobs:
+        assert torch.equal(want.slot, got.slot) and torch.equal(want.row_start, got.row_start)
+        assert torch.equal(want.free_left, got.free_left)
+
+
 # ------------------------------------------------------------------ stores
 @pytest.mark.parametrize("d", [128, 512])
 @pytest.mark.parametrize("extras", ["none", "norm", "rope", "both"])
@@ -746,3 +782,56 @@ def test_released_requests_give_their_pages_back():
     assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
     loop.step(i32([T, T]), [torch.cat([x, x])[:T]], [torch.cat([gate, gate])[:T]], [q])
     assert loop.missing() > 0                            # two requests do not fit: reported, not written elsewhere
+
+
+@pytest.mark.parametrize("d,H", [(128, 8), (512, 64)])
+def test_a_captured_step_replays_with_other_lengths(d, H):
+    """One captured step (padded to 70 rows) replayed with each step's lengths:
+    the bytes of the steps run one by one; rows past the last stay as they were."""
+    from long_context_attention_hca_b200.pipeline import PagedLoop
+    g = gen(77 + d)
+    B, N = 3, 70
+    bias = torch.randn((128, d), generator=g, device=DEV) * 0.5
+
+    def make():
+        loop = PagedLoop(B, H, LAYOUTS[d], [128, 0], 32, 2, max_tokens=400, max_rows=N, softmax_scale=d ** -0.5,
+                         token_page=16, entry_page=1)
+        loop.set_bias(0, bias)
+        return loop
+
+    x, gate, q = ([torch.zeros(s, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+                  for s in ((N, d), (N, d), (N, H, d)))
+    new = torch.zeros((B,), dtype=torch.int32, device=DEV)
+    eager, replayed = make(), make()
+    torch.cuda.synchronize()
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        outs = replayed.step(new, x, gate, q)
+    torch.cuda.synchronize()
+    for lens in ([70, 0, 0], [0, 60, 10], [57, 9, 1], [1, 1, 1], [0, 0, 0], [3, 66, 1], [1, 0, 1]):
+        for t in x + gate + q:
+            t.copy_(bf(tuple(t.shape), g))
+        new.copy_(i32(lens))
+        for o in outs:
+            o.fill_(7.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        want = eager.step(new, x, gate, q)
+        n = sum(lens)
+        for a, b in zip(want, outs):
+            assert torch.equal(a[:n], b[:n]) and bool((b[n:] == 7.0).all())
+    assert replayed.ctx.tolist() == eager.ctx.tolist() and replayed.missing() == eager.missing() == 0
+    assert torch.equal(replayed.token_table, eager.token_table)
+    assert torch.equal(replayed.layers[0].cache.codes, eager.layers[0].cache.codes)
+
+
+def test_a_negative_length_adds_nothing():
+    from long_context_attention_hca_b200.pipeline import PagedLoop
+    d, H = 128, 8
+    g = gen(3)
+    loop = PagedLoop(2, H, LAYOUTS[d], [0], 32, 0, max_tokens=64, max_rows=64, softmax_scale=d ** -0.5, token_page=16)
+    for lens, ctx in (([5, 2], [5, 2]), ([-3, 4], [5, 6])):
+        n = sum(max(v, 0) for v in lens)
+        loop.step(i32(lens), [bf((n, d), g)], [None], [bf((n, H, d), g)])
+        assert loop.ctx.tolist() == ctx
