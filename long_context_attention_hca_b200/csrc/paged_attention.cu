@@ -26,7 +26,16 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
 // (rg, kg) computes S for 16 rows and its TK / KG keys over all D dims (mma.sync,
 // fp16 operands, fp32 sums), the groups share row maxima and P through shared
 // memory, and warp (rg, kg) then accumulates its D / KG dims of O in registers.
-// Keys cross from their pages as stored and become fp16 in shared memory.
+// Keys cross from their pages as stored and become fp16 in shared memory.  With
+// R = 128 (d = 128 only: O of 16 rows and all dims fits a warp) there is one key
+// group: nothing of the softmax is shared, and a key is converted for twice as
+// many rows.
+//
+// Bound at d = 128: latency and issue, not bytes.  A 64-key tile of R = 128 takes
+// 9.3K clocks with one CTA an SM (1.5K converting keys, 1.1K queueing copies,
+// 2.1K S, 4.1K softmax and O) and 11K with two, 4096 tokens x 64 heads over 64K
+// take 516 us, 168 TFLOP/s; 33 single tokens of 8 heads, 10.7 us.  Converting
+// from registers a tile ahead and four-warp CTAs, three an SM, were no faster.
 //
 // A key that holds an infinity or a NaN (or a value beyond fp16's range) is
 // stored as zeros and marked: a query that sees it gets NaN, one that does not
@@ -43,7 +52,7 @@ struct Rows {
     static constexpr int DN = D - DR;
     static constexpr size_t Q_BYTES = size_t(R) * D * 2;
     static constexpr size_t K_BYTES = size_t(TK) * D * 2;
-    static constexpr size_t P_BYTES = size_t(R) * TK * 2;
+    static constexpr size_t P_BYTES = KG > 1 ? size_t(R) * TK * 2 : 0;
     static constexpr size_t CS_BYTES = size_t(R) * (DR / 2) * 8;     // cos / sin of each row's position
     static constexpr size_t RAW_BYTES = size_t(TK) * D * 2;          // the next tile's keys as stored
     static constexpr size_t SC_BYTES = size_t(TK) * 8 * 4;           // and their scales
@@ -112,7 +121,8 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
     const int t_begin = static_cast<int>(static_cast<int64_t>(n_tiles) * split / p.n_splits);
     const int t_end = static_cast<int>(static_cast<int64_t>(n_tiles) * (split + 1) / p.n_splits);
 
-    // ---- queries as stored, into the key buffer (not in use yet); a lane copies what it will convert
+    // ---- queries as stored, to where their fp16 rows go (converted in place, row by row); a lane copies what it will
+    // convert
     constexpr int CL = D / 32;                   // consecutive dims of a lane
     const uint32_t raw_a = static_cast<uint32_t>(__cvta_generic_to_shared(raw));
     const uint32_t sc_a = static_cast<uint32_t>(__cvta_generic_to_shared(s_sc));
@@ -120,10 +130,10 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
     for (int r = warp; r < T.rows; r += 8) {
         const uint16_t* src = p.q + (T.row0 + r) * D + lane * CL;
         if constexpr (CL >= 8) {
-            cp16(ka + r * (D * 2) + lane * 32, src);
-            cp16(ka + r * (D * 2) + lane * 32 + 16, src + 8);
+            cp16(qa + r * (D * 2) + lane * 32, src);
+            cp16(qa + r * (D * 2) + lane * 32 + 16, src + 8);
         } else {
-            cp8(ka + r * (D * 2) + lane * 8, src);
+            cp8(qa + r * (D * 2) + lane * 8, src);
         }
     }
     cp_commit();
@@ -196,11 +206,12 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
             if constexpr (CL >= 8) {
 #pragma unroll
                 for (int i = 0; i < CL / 8; ++i)
-                    *reinterpret_cast<uint4*>(v + 4 * i) = *reinterpret_cast<const uint4*>(ks + r * (D * 2) + lane * 32 + i * 16);
+                    *reinterpret_cast<uint4*>(v + 4 * i) = *reinterpret_cast<const uint4*>(qs + r * (D * 2) + lane * 32 + i * 16);
             } else {
-                *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(ks + r * (D * 2) + lane * 8);
+                *reinterpret_cast<uint2*>(v) = *reinterpret_cast<const uint2*>(qs + r * (D * 2) + lane * 8);
             }
         }
+        __syncwarp();                            // the row has been read
         float f[CL];
 #pragma unroll
         for (int i = 0; i < CL / 2; ++i) {
@@ -251,6 +262,7 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
 #pragma unroll
     for (int j = 0; j < C::NO; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
     float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.0f, 0.0f};
+    const int e_all = static_cast<int>(entries_before(p, T.ctx + T.r0 / p.H));       // entries that every row sees
 
     for (int t = t_begin; t < t_end; ++t) {
         cp_wait<0>();
@@ -289,94 +301,167 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
         flagged = __syncthreads_or(flagged);
         look_up(t + 2);
 
-        // ---- S = Q K^T for 16 rows and this warp's keys
-        float s[C::NT][4];
-#pragma unroll
-        for (int j = 0; j < C::NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
         const int mi = lane >> 3;
-#pragma unroll 8
-        for (int kk = 0; kk < D / 16; ++kk) {
-            uint32_t a[4];
-            ldsm4(qa + swz<D * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
-            if constexpr (C::NT >= 2) {
+        if constexpr (C::KG == 1) {
+            // A row's softmax stays in its warp: 32 keys at a time (S of 64 would not fit the registers beside O), P
+            // from registers straight into the second product, no mask where every row sees the whole tile.
+            const bool masked = flagged || (t + 1) * TK > e_all;
+#pragma unroll 1
+            for (int k0 = 0; k0 < TK; k0 += 32) {
+                float s[4][4];
 #pragma unroll
-                for (int nt = 0; nt < C::NT; nt += 2) {
-                    uint32_t b[4];
-                    ldsm4(ka + swz<D * 2>(kg * C::KEYS + nt * 8 + (lane & 7) + 8 * (mi >> 1), 2 * kk + (mi & 1)), b);
-                    mma16816(s[nt], a, b[0], b[1]);
-                    mma16816(s[nt + 1], a, b[2], b[3]);
+                for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t a[4];
+                    ldsm4(qa + swz<D * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
+#pragma unroll
+                    for (int nt = 0; nt < 4; nt += 2) {
+                        uint32_t b[4];
+                        ldsm4(ka + swz<D * 2>(k0 + nt * 8 + (lane & 7) + 8 * (mi >> 1), 2 * kk + (mi & 1)), b);
+                        mma16816(s[nt], a, b[0], b[1]);
+                        mma16816(s[nt + 1], a, b[2], b[3]);
+                    }
                 }
-            } else {
-                // 8 keys: one x4 load brings two k-steps; the odd step uses the pair loaded with the even one
-                uint32_t b[4];
-                ldsm4(ka + swz<D * 2>(kg * 8 + (lane & 7), (2 * (kk & ~1) + mi)), b);
-                mma16816(s[0], a, (kk & 1) ? b[2] : b[0], (kk & 1) ? b[3] : b[1]);
+                if (masked)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = k0 + j * 8 + q4 * 2 + (i & 1);
+                            s[j][i] = sees(rk[i >> 1], T.n_e, t * TK + key) ? s[j][i] + s_add[key] : -INFINITY;
+                        }
+                float alpha[2], ref[2], rs[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) mx = fmaxf(mx, fmaxf(s[j][2 * i], s[j][2 * i + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m_r[i], mx * p.scale_log2);
+                    alpha[i] = mn == -INFINITY ? 1.0f : ex2(m_r[i] - mn);
+                    m_r[i] = mn;
+                    ref[i] = mn == -INFINITY ? 0.0f : mn;
+                }
+                uint32_t pr[4][2];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        pr[j][i] = pack_half2(ex2(fmaf(s[j][2 * i], p.scale_log2, -ref[i])), ex2(fmaf(s[j][2 * i + 1], p.scale_log2, -ref[i])));
+                        const float2 f = unpack_half2(pr[j][i]);     // l sums the probabilities as PV uses them
+                        rs[i] += f.x + f.y;
+                    }
+                l_r[0] = l_r[0] * alpha[0] + rs[0];
+                l_r[1] = l_r[1] * alpha[1] + rs[1];
+                if (__any_sync(0xffffffffu, alpha[0] != 1.0f || alpha[1] != 1.0f))
+#pragma unroll
+                    for (int j = 0; j < C::NO; ++j) {
+                        o[j][0] *= alpha[0]; o[j][1] *= alpha[0];
+                        o[j][2] *= alpha[1]; o[j][3] *= alpha[1];
+                    }
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {
+                    const uint32_t a[4] = {pr[2 * kk][0], pr[2 * kk][1], pr[2 * kk + 1][0], pr[2 * kk + 1][1]};
+#pragma unroll
+                    for (int nt = 0; nt < C::NO; nt += 2) {
+                        uint32_t b[4];
+                        ldsm4t(ka + swz<D * 2>(k0 + kk * 16 + (lane & 7) + 8 * (mi & 1), nt + (mi >> 1)), b);
+                        mma16816(o[nt], a, b[0], b[1]);
+                        mma16816(o[nt + 1], a, b[2], b[3]);
+                    }
+                }
             }
-        }
-        // ---- logits (base 2), masks, row maxima over the key groups
-        float mx[2] = {-INFINITY, -INFINITY};
+        } else {
+            // ---- S = Q K^T for 16 rows and this warp's keys
+            float s[C::NT][4];
 #pragma unroll
-        for (int j = 0; j < C::NT; ++j)
+            for (int j = 0; j < C::NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+#pragma unroll 8
+            for (int kk = 0; kk < D / 16; ++kk) {
+                uint32_t a[4];
+                ldsm4(qa + swz<D * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
+                if constexpr (C::NT >= 2) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int key = kg * C::KEYS + j * 8 + q4 * 2 + (i & 1);
-                float v = s[j][i] * p.scale_log2;
-                if (flagged) v += s_add[key];
-                if (!sees(rk[i >> 1], T.n_e, t * TK + key)) v = -INFINITY;
-                s[j][i] = v;
-                mx[i >> 1] = fmaxf(mx[i >> 1], v);
+                    for (int nt = 0; nt < C::NT; nt += 2) {
+                        uint32_t b[4];
+                        ldsm4(ka + swz<D * 2>(kg * C::KEYS + nt * 8 + (lane & 7) + 8 * (mi >> 1), 2 * kk + (mi & 1)), b);
+                        mma16816(s[nt], a, b[0], b[1]);
+                        mma16816(s[nt + 1], a, b[2], b[3]);
+                    }
+                } else {
+                    // 8 keys: one x4 load brings two k-steps; the odd step uses the pair loaded with the even one
+                    uint32_t b[4];
+                    ldsm4(ka + swz<D * 2>(kg * 8 + (lane & 7), (2 * (kk & ~1) + mi)), b);
+                    mma16816(s[0], a, (kk & 1) ? b[2] : b[0], (kk & 1) ? b[3] : b[1]);
+                }
+            }
+            // ---- logits (base 2), masks, row maxima over the key groups
+            float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < C::NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int key = kg * C::KEYS + j * 8 + q4 * 2 + (i & 1);
+                    float v = s[j][i] * p.scale_log2;
+                    if (flagged) v += s_add[key];
+                    if (!sees(rk[i >> 1], T.n_e, t * TK + key)) v = -INFINITY;
+                    s[j][i] = v;
+                    mx[i >> 1] = fmaxf(mx[i >> 1], v);
+                }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+                mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            }
+            if (q4 == 0) { s_max[warp][g8] = mx[0]; s_max[warp][g8 + 8] = mx[1]; }
+            __syncthreads();
+            float alpha[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float mn = m_r[i];
+#pragma unroll
+                for (int k = 0; k < C::KG; ++k) mn = fmaxf(mn, s_max[rg * C::KG + k][g8 + 8 * i]);
+                // nothing seen yet: any finite reference does (every term is 0)
+                alpha[i] = mn == -INFINITY ? 1.0f : ex2(m_r[i] - mn);
+                m_r[i] = mn;
+            }
+            float rs[2] = {0.0f, 0.0f};
+            const float ref[2] = {m_r[0] == -INFINITY ? 0.0f : m_r[0], m_r[1] == -INFINITY ? 0.0f : m_r[1]};
+#pragma unroll
+            for (int j = 0; j < C::NT; ++j) {
+                const uint32_t lo = pack_half2(ex2(s[j][0] - ref[0]), ex2(s[j][1] - ref[0]));
+                const uint32_t hi = pack_half2(ex2(s[j][2] - ref[1]), ex2(s[j][3] - ref[1]));
+                // l sums the probabilities as PV uses them: fp16, at most half a step off each
+                const float2 fl = unpack_half2(lo), fh = unpack_half2(hi);
+                rs[0] += fl.x + fl.y;
+                rs[1] += fh.x + fh.y;
+                const int col = kg * C::KEYS + j * 8 + q4 * 2;
+                const int r = rg * 16 + g8;
+                *reinterpret_cast<uint32_t*>(ps + swz<TK * 2>(r, col >> 3) + (col & 7) * 2) = lo;
+                *reinterpret_cast<uint32_t*>(ps + swz<TK * 2>(r + 8, col >> 3) + (col & 7) * 2) = hi;
             }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        }
-        if (q4 == 0) { s_max[warp][g8] = mx[0]; s_max[warp][g8 + 8] = mx[1]; }
-        __syncthreads();
-        float alpha[2];
+            for (int i = 0; i < 2; ++i) l_r[i] = l_r[i] * alpha[i] + rs[i];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float mn = m_r[i];
+            for (int j = 0; j < C::NO; ++j) {
+                o[j][0] *= alpha[0]; o[j][1] *= alpha[0];
+                o[j][2] *= alpha[1]; o[j][3] *= alpha[1];
+            }
+            __syncthreads();                         // P is complete
+            // ---- O += P V (the same tile), this warp's dims
 #pragma unroll
-            for (int k = 0; k < C::KG; ++k) mn = fmaxf(mn, s_max[rg * C::KG + k][g8 + 8 * i]);
-            // nothing seen yet: any finite reference does (every term is 0)
-            alpha[i] = mn == -INFINITY ? 1.0f : ex2(m_r[i] - mn);
-            m_r[i] = mn;
-        }
-        float rs[2] = {0.0f, 0.0f};
-        const float ref[2] = {m_r[0] == -INFINITY ? 0.0f : m_r[0], m_r[1] == -INFINITY ? 0.0f : m_r[1]};
+            for (int kk = 0; kk < TK / 16; ++kk) {
+                uint32_t a[4];
+                ldsm4(pa + swz<TK * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
 #pragma unroll
-        for (int j = 0; j < C::NT; ++j) {
-            const uint32_t lo = pack_half2(ex2(s[j][0] - ref[0]), ex2(s[j][1] - ref[0]));
-            const uint32_t hi = pack_half2(ex2(s[j][2] - ref[1]), ex2(s[j][3] - ref[1]));
-            // l sums the probabilities as PV uses them: fp16, at most half a step off each
-            const float2 fl = unpack_half2(lo), fh = unpack_half2(hi);
-            rs[0] += fl.x + fl.y;
-            rs[1] += fh.x + fh.y;
-            const int col = kg * C::KEYS + j * 8 + q4 * 2;
-            const int r = rg * 16 + g8;
-            *reinterpret_cast<uint32_t*>(ps + swz<TK * 2>(r, col >> 3) + (col & 7) * 2) = lo;
-            *reinterpret_cast<uint32_t*>(ps + swz<TK * 2>(r + 8, col >> 3) + (col & 7) * 2) = hi;
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) l_r[i] = l_r[i] * alpha[i] + rs[i];
-#pragma unroll
-        for (int j = 0; j < C::NO; ++j) {
-            o[j][0] *= alpha[0]; o[j][1] *= alpha[0];
-            o[j][2] *= alpha[1]; o[j][3] *= alpha[1];
-        }
-        __syncthreads();                         // P is complete
-        // ---- O += P V (the same tile), this warp's dims
-#pragma unroll
-        for (int kk = 0; kk < TK / 16; ++kk) {
-            uint32_t a[4];
-            ldsm4(pa + swz<TK * 2>(rg * 16 + (lane & 7) + 8 * (mi & 1), 2 * kk + (mi >> 1)), a);
-#pragma unroll
-            for (int nt = 0; nt < C::NO; nt += 2) {
-                uint32_t b[4];
-                ldsm4t(ka + swz<D * 2>(kk * 16 + (lane & 7) + 8 * (mi & 1), kg * (C::DW / 8) + nt + (mi >> 1)), b);
-                mma16816(o[nt], a, b[0], b[1]);
-                mma16816(o[nt + 1], a, b[2], b[3]);
+                for (int nt = 0; nt < C::NO; nt += 2) {
+                    uint32_t b[4];
+                    ldsm4t(ka + swz<D * 2>(kk * 16 + (lane & 7) + 8 * (mi & 1), kg * (C::DW / 8) + nt + (mi >> 1)), b);
+                    mma16816(o[nt], a, b[0], b[1]);
+                    mma16816(o[nt + 1], a, b[2], b[3]);
+                }
             }
         }
     }
@@ -560,8 +645,14 @@ constexpr int64_t MAX_STAGE_ROWS = 2ll << 20;
 constexpr int PAIR_ROWS = 128;
 
 // Rows of a row kernel's tile: 16 when no request can fill more (a small head
-// count at decode), else 64.
-inline int tile_rows(int64_t max_new, int H) { return max_new * H <= 16 ? 16 : 64; }
+// count at decode); 128 when such tiles give every SM one (500 tokens x 64 heads
+// over 64K: 77 us, with 64 rows 94; 4096 tokens 516 and 650; between one and two
+// tiles an SM either is ahead by turns, 4 x 170 window tokens 65 and 58 us); else
+// 64 (64 tokens over 128K: 41 us; 32 single tokens 26, splits included).
+inline int tile_rows(int64_t n_rows, int64_t max_new, int H) {
+    if (max_new * H <= 16) return 16;
+    return n_rows * H / 128 >= sm_count() ? 128 : 64;
+}
 inline int64_t tile_count(int64_t n_rows, int H, int B, int R) { return n_rows * H / R + B; }
 
 // Splits: enough work for every SM (pair) when the tiles alone are too few, but
@@ -588,7 +679,7 @@ static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int6
     const int64_t stage_rows = tc_stage_rows(n_rows, B, max_entries, W, n_first);
     const int64_t reqs = n_rows < B ? n_rows : B;      // requests that can have a new token
     k.pairs = D == 512 && stage_rows <= MAX_STAGE_ROWS;
-    k.R = k.pairs ? PAIR_ROWS : (D == 512 ? 64 : tile_rows(max_new, H));
+    k.R = k.pairs ? PAIR_ROWS : (D == 512 ? 64 : tile_rows(n_rows, max_new, H));
     k.tiles = tile_count(n_rows, H, B, k.R);
     // tiles that can hold rows: one a request when no request fills more
     const int64_t busy = max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs;
@@ -622,7 +713,8 @@ static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     kern<<<dim3(static_cast<unsigned>(k.tiles), k.splits), 256, Rows<D, R>::SMEM, st>>>(p);
     HCA_CHECK_LAUNCH();
-    return launch_combine<D, R>(p, k, st);
+    if constexpr (R == 128) return HCA_OK;       // (never split)
+    else return launch_combine<D, R>(p, k, st);
 }
 
 }  // namespace paged
@@ -647,6 +739,7 @@ int paged_attn_launch(paged::Params p, int D, int64_t max_new, int64_t max_entri
         return rc == HCA_OK ? paged::launch_combine<512, paged::PAIR_ROWS>(p, k, st) : rc;
     }
     if (D == 512) return paged::launch_rows<512, 64>(p, k, st);
+    if (k.R == 128) return paged::launch_rows<128, 128>(p, k, st);
     return k.R == 16 ? paged::launch_rows<128, 16>(p, k, st) : paged::launch_rows<128, 64>(p, k, st);
 }
 

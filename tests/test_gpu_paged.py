@@ -835,3 +835,42 @@ def test_a_negative_length_adds_nothing():
         n = sum(max(v, 0) for v in lens)
         loop.step(i32(lens), [bf((n, d), g)], [None], [bf((n, H, d), g)])
         assert loop.ctx.tolist() == ctx
+
+
+# ------------------------------------------------------------------ d = 128, steps of many rows (tiles of 128)
+MANY_ROWS = [
+    dict(d=128, H=128, ctx=[90, 700, 0], new=[150, 170, 21], W=17, m=4, PE=7, PT=9),
+    dict(d=128, H=128, ctx=[500, 1, 60], new=[200, 111, 1], W=100, n_first=64, extras=True),
+    dict(d=128, H=100, ctx=[2000, 3], new=[370, 40], W=128, m=128, extras=True, PE=5),
+    dict(d=128, H=128, ctx=[0], new=[310], W=1, m=4),
+]
+
+
+@pytest.mark.parametrize("k", range(len(MANY_ROWS)))
+def test_many_rows(k):
+    c = Case(seed=40 + k, **MANY_ROWS[k])
+    out = torch.full_like(c.q, 7.0)
+    got = c.run(out=out, max_new=max(c.new))
+    assert torch.all(got[c.N:] == 7.0)
+    c.check(got, rows=[n for n in range(c.N) if n % 7 == 0 or n in (c.N - 1, 150, 149, 200, 201)])
+
+
+def test_many_rows_non_finite_keys_and_missing_pages():
+    a = dict(d=128, H=128, ctx=[300, 200], new=[290, 30], W=20, m=4, PT=8)
+    c, ref = Case(seed=50, **a), Case(seed=50, **a)
+    clean = c.run()
+    c.etab[0, 2] = -1                                    # entries 32..47 of request 0
+    c.ttab[1, :], c.etab[1, :] = -1, c.cache.B           # request 1 sees nothing
+    got = c.run()
+    keys = ref.keys
+    ref.keys = lambda b, p: (np.delete(keys(b, p)[0], np.arange(32, 48)), keys(b, p)[1])
+    ref.check(got, rows=[0, 1, 63, 64, 200, 289])
+    assert torch.all(got[290:320] == 0)
+    c = Case(seed=50, **a)
+    c.pages.view(-1, 128)[int(c.ttab[0, 400 // 8]) * 8 + 400 % 8, 3] = float("inf")     # seen at 400 .. 419
+    got = c.run()
+    for i in range(320):
+        if 100 <= i < 120:
+            assert torch.isnan(got[i]).all()
+        else:
+            assert torch.equal(got[i], clean[i])
