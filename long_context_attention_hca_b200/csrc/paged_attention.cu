@@ -535,6 +535,7 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
 // loads, so four warps share a row: each takes every fourth split, its lanes
 // over the dims, eight splits' loads in flight; the four sums meet in shared
 // memory.  Lane s of every warp holds split s's weight (twice for S > 32).
+// Measured: 4 tokens x 64 heads in 18 splits 6.7 us, 33 x 8 in 6 splits 5 us (cold).
 template <int D, int R>
 __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
     constexpr int DR = D == 512 ? 64 : 32, DN = D - DR, CL = D / 32;
