@@ -874,3 +874,56 @@ def test_many_rows_non_finite_keys_and_missing_pages():
             assert torch.isnan(got[i]).all()
         else:
             assert torch.equal(got[i], clean[i])
+
+
+# ------------------------------------------------------------------ positions up to 2^31
+TOP = 1 << 31
+
+
+@pytest.mark.parametrize("d,H,extras,m", [(512, 64, False, 0), (512, 64, True, 0), (128, 8, True, 0), (128, 8, True, 128),
+                                          (512, 64, True, 128)])
+def test_attention_at_the_last_positions(d, H, extras, m):
+    """Positions right below 2^31: the first column and the last ones of a wide table hold pages, all others none."""
+    PT, PE, W, new = 256, 16, 64, 7
+    c = Case(d, H, [300], [new], W, m=m, n_first=0 if m else 4, PT=PT, PE=PE, extras=extras, seed=60)
+    pages = c.ttab[0].clone()
+    c.ttab = torch.full((1, TOP // PT), -1, dtype=torch.int32, device=DEV)
+    c.ttab[0, 0] = pages[0]
+    c.ttab[0, -2:] = pages[:2]
+    c.ctx = [TOP - new - 1]                              # the last query at 2^31 - 2
+    if m:
+        cols = TOP // m // PE
+        c.etab = torch.full((1, cols), -1, dtype=torch.int32, device=DEV)
+        c.etab[0, 3] = 0
+        c.etab[0, cols - 1] = c.cache.B - 1
+        keys = c.keys
+
+        def present(b, p):
+            c.m = 0                                      # the tokens alone; entries by hand
+            rt = keys(b, p)[1]
+            c.m = m
+            n_e = (p + 1) // m
+            return np.array([i for i in range(PE)] + [(c.cache.B - 1) * PE + i for i in range(PE)
+                                                      if (cols - 1) * PE + i < n_e]), rt
+        c.keys = present
+    c.check(c.run(max_new=new))
+
+
+def test_plan_and_store_at_the_last_positions():
+    d, P, new = 128, 256, 300
+    g = gen(8)
+    width = TOP // P
+    ctx = TOP - 1 - new
+    table = torch.full((1, width), -1, dtype=torch.int32, device=DEV)
+    table[0, ctx // P] = 2
+    plan = hca.kv_page_plan(i32([ctx]), i32([new]), 1, P, table, i32([0, 1]), i32([2]), max_rows=new)
+    pos = np.arange(ctx, ctx + new)
+    page = np.where(pos // P == ctx // P, 2, 1 - (pos // P - ctx // P - 1))
+    assert plan.row_pos.tolist() == pos.tolist() and plan.slot.tolist() == (page * P + pos % P).tolist()
+    assert plan.missing.item() == 0 and plan.free_left.item() == 2 - ((ctx + new - 1) // P - ctx // P)
+    x = bf((new, d), g)
+    fr = inp.rope_inv_freq(32, device=DEV)
+    pool = torch.zeros((3, P, d), dtype=torch.bfloat16, device=DEV)
+    hca.kv_page_store(x, plan, pool, LAYOUTS[d], extras=hca.EntryExtras(None, 0.0, fr))
+    want = oracle.token_prep(host(x), pos, 32, inv_freq=host(fr))
+    assert np.array_equal(host(pool).reshape(-1, d)[plan.slot.cpu().numpy()], want)
