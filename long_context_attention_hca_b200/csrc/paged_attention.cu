@@ -649,7 +649,7 @@ constexpr int PAIR_ROWS = 128;
 // count at decode); 128 when such tiles give every SM one (500 tokens x 64 heads
 // over 64K: 77 us, with 64 rows 94; 4096 tokens 516 and 650; between one and two
 // tiles an SM either is ahead by turns, 4 x 170 window tokens 65 and 58 us); else
-// 64 (64 tokens over 128K: 41 us; 32 single tokens 26, splits included).
+// 64 (64 tokens over 128K: 35 us; 32 single tokens 23, splits included).
 inline int tile_rows(int64_t n_rows, int64_t max_new, int H) {
     if (max_new * H <= 16) return 16;
     return n_rows * H / 128 >= sm_count() ? 128 : 64;
@@ -688,7 +688,11 @@ static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int6
         k.stage_bytes = tc_stage_bytes(stage_rows, n_rows);
         k.splits = split_count(sm_count() / 2, busy, max_keys, 128, 5);
     } else {
-        k.splits = split_count(sm_count(), busy, max_keys, TK, 2);
+        // d = 128: two CTAs fit an SM, where that gives shorter chains and not the same work twice as thin (32 single
+        // tokens x 64 heads over 64K: 22.6 us with both slots counted, 26.1 with one; 100 over 32K: 37 and 30 us, so
+        // not for 64-row tiles that fill more than half the SMs; with 8 heads 16.7 and 20.4)
+        const bool both = D == 128 && (k.R == 16 || 2 * busy <= sm_count());
+        k.splits = split_count(both ? 2 * sm_count() : sm_count(), busy, max_keys, TK, 2);
     }
     return k;
 }
