@@ -34,7 +34,7 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
 // Bound at d = 128: latency and issue, not bytes.  A 64-key tile of R = 128 takes
 // 9.3K clocks with one CTA an SM (1.5K converting keys, 1.1K queueing copies,
 // 2.1K S, 4.1K softmax and O) and 11K with two, 4096 tokens x 64 heads over 64K
-// take 516 us, 168 TFLOP/s; 33 single tokens of 8 heads, 10.7 us.  Converting
+// take 509 us, 171 TFLOP/s; 33 single tokens of 8 heads, 10.7 us.  Converting
 // from registers a tile ahead and four-warp CTAs, three an SM, were no faster.
 //
 // A key that holds an infinity or a NaN (or a value beyond fp16's range) is
@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
     };
     auto copy_tile = [&](int t) {
 #pragma unroll 2
-        for (int key = kr; key < TK; key += KPP) {
+        for (int k = 0; k < TK / KPP; ++k) {
+            const int key = kr + k * KPP;
             const int64_t row = s_row[t & 1][key];
             if (row < 0) continue;
             const uint32_t dst = raw_a + key * (D * 2) + u * 32;
@@ -269,7 +270,8 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
         __syncthreads();                         // the last tile's keys and P are read
         bool flagged = false;
 #pragma unroll 2
-        for (int key = kr; key < TK; key += KPP) {
+        for (int k = 0; k < TK / KPP; ++k) {
+            const int key = kr + k * KPP;
             const int slot = t * TK + key;
             const bool here = s_row[t & 1][key] >= 0;
             uint32_t h[8];
@@ -647,8 +649,8 @@ constexpr int PAIR_ROWS = 128;
 
 // Rows of a row kernel's tile: 16 when no request can fill more (a small head
 // count at decode); 128 when such tiles give every SM one (500 tokens x 64 heads
-// over 64K: 77 us, with 64 rows 94; 4096 tokens 516 and 650; between one and two
-// tiles an SM either is ahead by turns, 4 x 170 window tokens 65 and 58 us); else
+// over 64K: 76 us, with 64 rows 94; 4096 tokens 509 and 650; between one and two
+// tiles an SM either is ahead by turns, 4 x 170 window tokens 63 and 58 us); else
 // 64 (64 tokens over 128K: 35 us; 32 single tokens 23, splits included).
 inline int tile_rows(int64_t n_rows, int64_t max_new, int H) {
     if (max_new * H <= 16) return 16;
