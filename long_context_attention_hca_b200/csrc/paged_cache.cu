@@ -310,18 +310,20 @@ __device__ __forceinline__ CompItem comp_item(const CompArgs& a, int64_t it) {
 // m = 128: few entries complete per step (16K tokens are 120), so an item is
 // spread over a cluster of d / 64 CTAs of 64 channels each, and inside a CTA
 // over the tokens: warp w takes tokens w, w + 8, ... (16 of them, every load of
-// gate and x in flight at once), the terms e_i and e_i x_i go through shared
-// memory, and one thread per channel adds them up in order.  One thread per two
+// gate and x in flight at once), e_i and x_i go through shared memory, and one
+// thread per channel adds e_i and e_i x_i up in order.  One thread per two
 // channels for all 128 tokens (the form of m = 4) took 40 us for 16K tokens of d
-// = 512, a round trip to DRAM for every batch of loads; this takes 30 us (1.1
-// TB/s), bound by issue (31-41% of the slots) and the ordered sums: one warp pair of
-// eight adds while the others are done, and shared memory holds 3 CTAs an SM.  With RMSNorm the CTAs'
+// = 512, a round trip to DRAM for every batch of loads; this takes 24.7 us (1.4
+// TB/s), bound by issue (the exponentials) and the ordered sums, for which one warp
+// pair of eight is at work.  x as stored in shared memory and 64 registers let four
+// CTAs share an SM (e_i x_i there and 80 registers: three, 30.3 us). With RMSNorm the CTAs'
 // sums of squares meet through distributed shared memory, in the C ABI's tree.
 template <int D>
-__global__ void __cluster_dims__(D / 64, 1, 1) __launch_bounds__(256)
+__global__ void __cluster_dims__(D / 64, 1, 1) __launch_bounds__(256, 4)
 page_compress128_kernel(CompArgs a) {
     constexpr int M = 128, G = D / 64, TW = M / 8;
-    extern __shared__ float2 terms[];           // [M][64]: e_i, e_i x_i
+    extern __shared__ float terms[];            // [M][64] e_i, then [M][64] x_i as stored
+    uint16_t* const xs = reinterpret_cast<uint16_t*>(terms + M * 64);
     __shared__ float s_max[8][64];
     __shared__ float s_sum[2], s_all[G];
     __shared__ CosSin s_cs[32];                 // of the entry's position, in the CTA that holds the RoPE dims
@@ -346,6 +348,8 @@ page_compress128_kernel(CompArgs a) {
             gz[j] = *reinterpret_cast<const uint32_t*>((old ? a.tail_gate : a.gate) + off);
             xv[j] = *reinterpret_cast<const uint32_t*>((old ? a.tail_x : a.x) + off);
         }
+#pragma unroll
+        for (int j = 0; j < TW; ++j) *reinterpret_cast<uint32_t*>(xs + (warp + 8 * j) * 64 + 2 * lane) = xv[j];
         float2 z[TW];
         float m0 = -INFINITY, m1 = -INFINITY;
 #pragma unroll
@@ -366,9 +370,8 @@ page_compress128_kernel(CompArgs a) {
         }
 #pragma unroll
         for (int j = 0; j < TW; ++j) {
-            const float2 x = bf2(xv[j]);
             const float e0 = cw_exp_neg(__fsub_rn(z[j].x, m0)), e1 = cw_exp_neg(__fsub_rn(z[j].y, m1));
-            *reinterpret_cast<float4*>(&terms[(warp + 8 * j) * 64 + 2 * lane]) = make_float4(e0, __fmul_rn(e0, x.x), e1, __fmul_rn(e1, x.y));
+            *reinterpret_cast<float2*>(&terms[(warp + 8 * j) * 64 + 2 * lane]) = make_float2(e0, e1);
         }
         __syncthreads();                        // (the tail rows have been read, too)
         float y = 0.0f;
@@ -378,9 +381,9 @@ page_compress128_kernel(CompArgs a) {
             float S = 0.0f, N = 0.0f;
 #pragma unroll 16
             for (int i = 0; i < M; ++i) {
-                const float2 t = terms[i * 64 + tid];
-                S = __fadd_rn(S, t.x);
-                N = __fadd_rn(N, t.y);
+                const float e = terms[i * 64 + tid];
+                S = __fadd_rn(S, e);
+                N = __fadd_rn(N, __fmul_rn(e, __uint_as_float(static_cast<uint32_t>(xs[i * 64 + tid]) << 16)));
             }
             y = __fdiv_rn(N, S);
         }
@@ -607,7 +610,7 @@ int page_compress_launch(int m, const uint16_t* x, const uint16_t* gate, int64_t
         if (L.d == 512) page_compress_kernel<4, 512><<<grid, 256, 0, st>>>(a);
         else page_compress_kernel<4, 128><<<grid, 256, 0, st>>>(a);
     } else {
-        constexpr int smem = 128 * 64 * sizeof(float2);
+        constexpr int smem = 128 * 64 * (sizeof(float) + sizeof(uint16_t));
         auto kern = L.d == 512 ? page_compress128_kernel<512> : page_compress128_kernel<128>;
         const cudaError_t e = L.d == 512 ? allow_smem<page_compress128_kernel<512>>(smem) : allow_smem<page_compress128_kernel<128>>(smem);
         if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
