@@ -316,8 +316,9 @@ __device__ __forceinline__ CompItem comp_item(const CompArgs& a, int64_t it) {
 // = 512, a round trip to DRAM for every batch of loads; this takes 24.7 us (1.4
 // TB/s), bound by issue (the exponentials) and the ordered sums, for which one warp
 // pair of eight is at work.  x as stored in shared memory and 64 registers let four
-// CTAs share an SM (e_i x_i there and 80 registers: three, 30.3 us). With RMSNorm the CTAs'
-// sums of squares meet through distributed shared memory, in the C ABI's tree.
+// CTAs share an SM (e_i x_i there and 80 registers: three, 30.3 us).  With RMSNorm
+// the CTAs' sums of squares meet through distributed shared memory, in the C ABI's
+// tree.
 template <int D>
 __global__ void __cluster_dims__(D / 64, 1, 1) __launch_bounds__(256, 4)
 page_compress128_kernel(CompArgs a) {
