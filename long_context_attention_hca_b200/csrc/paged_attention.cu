@@ -651,10 +651,12 @@ constexpr int PAIR_ROWS = 128;
 // count at decode); 128 when such tiles give every SM one (500 tokens x 64 heads
 // over 64K: 76 us, with 64 rows 94; 4096 tokens 509 and 650; between one and two
 // tiles an SM either is ahead by turns, 4 x 170 window tokens 63 and 58 us); else
-// 64 (64 tokens over 128K: 35 us; 32 single tokens 23, splits included).
-inline int tile_rows(int64_t n_rows, int64_t max_new, int H) {
+// 64 (64 tokens over 128K: 35 us; 32 single tokens 23, splits included).  What
+// counts is the rows that can hold a query: a padded step has many others.
+inline int tile_rows(int64_t n_rows, int B, int64_t max_new, int H) {
     if (max_new * H <= 16) return 16;
-    return n_rows * H / 128 >= sm_count() ? 128 : 64;
+    const int64_t live = n_rows < B * max_new ? n_rows : B * max_new;
+    return live * H / 128 >= sm_count() ? 128 : 64;
 }
 inline int64_t tile_count(int64_t n_rows, int H, int B, int R) { return n_rows * H / R + B; }
 
@@ -682,13 +684,15 @@ static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int6
     const int64_t stage_rows = tc_stage_rows(n_rows, B, max_entries, W, n_first);
     const int64_t reqs = n_rows < B ? n_rows : B;      // requests that can have a new token
     k.pairs = D == 512 && stage_rows <= MAX_STAGE_ROWS;
-    k.R = k.pairs ? PAIR_ROWS : (D == 512 ? 64 : tile_rows(n_rows, max_new, H));
+    k.R = k.pairs ? PAIR_ROWS : (D == 512 ? 64 : tile_rows(n_rows, B, max_new, H));
     k.tiles = tile_count(n_rows, H, B, k.R);
     // tiles that can hold rows: one a request when no request fills more
     const int64_t busy = max_new * H <= k.R ? reqs : n_rows * H / k.R + reqs;
     if (k.pairs) {
         k.stage_bytes = tc_stage_bytes(stage_rows, n_rows);
         k.splits = split_count(sm_count() / 2, busy, max_keys, 128, 5);
+    } else if (k.R == 128) {
+        k.splits = 1;       // taken only where the tiles alone give every SM one: there is no combine of such tiles
     } else {
         // d = 128: two CTAs fit an SM, where that gives shorter chains and not the same work twice as thin (32 single
         // tokens x 64 heads over 64K: 22.6 us with both slots counted, 26.1 with one; 100 over 32K: 37 and 30 us, so
@@ -720,7 +724,7 @@ static int launch_rows(const Params& p, const Plan& k, cudaStream_t st) {
     if (e != cudaSuccess) { set_last_cuda_error(static_cast<int>(e)); return HCA_ERR_CUDA; }
     kern<<<dim3(static_cast<unsigned>(k.tiles), k.splits), 256, Rows<D, R>::SMEM, st>>>(p);
     HCA_CHECK_LAUNCH();
-    if constexpr (R == 128) return HCA_OK;       // (never split)
+    if constexpr (R == 128) return HCA_OK;       // (one split: make_plan)
     else return launch_combine<D, R>(p, k, st);
 }
 

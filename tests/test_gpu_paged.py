@@ -927,3 +927,24 @@ def test_plan_and_store_at_the_last_positions():
     hca.kv_page_store(x, plan, pool, LAYOUTS[d], extras=hca.EntryExtras(None, 0.0, fr))
     want = oracle.token_prep(host(x), pos, 32, inv_freq=host(fr))
     assert np.array_equal(host(pool).reshape(-1, d)[plan.slot.cpu().numpy()], want)
+
+
+# ------------------------------------------------------------------ d = 128, steps padded far beyond their live rows
+PADDED = [                                               # (case, rows of q, max_new)
+    (dict(H=64, ctx=[32766, 9000, 0, 20000, 511, 32766, 100, 16000], new=[1, 1, 1, 1, 0, 1, 1, 1], W=128, m=4, PE=64), 512, 1),
+    (dict(H=64, ctx=[32765, 9000, 0, 20000, 511, 32766, 100, 16000], new=[2, 1, 2, 0, 2, 1, 1, 2], W=128, m=4, PE=64), 512, 2),
+    (dict(H=64, ctx=[55 * b for b in range(74)], new=[1 + b % 2 for b in range(74)], W=128, m=4, extras=True), 296, 2),
+    (dict(H=128, ctx=[3800], new=[200], W=128, m=4), 200, 1),       # (a bound that is too small)
+    (dict(H=64, ctx=[5000, 2, 700, 0, 1023, 1024, 40, 3000], new=[2, 2, 1, 2, 0, 1, 2, 1], W=1024, n_first=4, extras=True), 512, 2),
+]
+
+
+@pytest.mark.parametrize("k", range(len(PADDED)))
+def test_padded_steps_write_every_live_row(k):
+    """Many rows of q, few of them live: every live row is written, whatever tiles and splits are chosen."""
+    kw, n, mn = PADDED[k]
+    c = Case(128, seed=70 + k, pad=n - sum(kw["new"]), **kw)
+    out = torch.full_like(c.q, 7.0)
+    got = c.run(out=out, max_new=mn)
+    assert torch.all(got[c.N:] == 7.0) and got.shape[0] == n
+    c.check(got, rows=[r for r in range(c.N) if r < 40 or r % 9 == 0 or r == c.N - 1])

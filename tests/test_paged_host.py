@@ -125,3 +125,25 @@ def test_workspace_sizes(lib):
     assert chunk(lib, ws=A, wb=need - 1, **long) == WORKSPACE
     assert size(0, 1, 64, L512, 0, 0, 128, 0) == 0
     assert size(5, 1, 0, L512, 0, 0, 128, 0) == 0 and size(5, 1, 64, Layout(1, 1, 1), 0, 0, 128, 0) == 0
+
+
+def test_every_split_has_rows_of_a_joined_tile(lib):
+    """d = 128: tiles of 128 rows are never split (nothing joins their splits).
+    Without staged keys the workspace is tiles x splits x rows x (128 fp16 + 2
+    fp32) and 256 bytes, so that its size tells the tile: nothing, or a whole
+    number of splits of 16- or 64-row tiles.  The first four: steps padded far
+    beyond their live rows, and a bound that is too small."""
+    size = lib.paged_attn_workspace_size
+    steps = [(512, 8, 64, 1, 8192, 128, 0), (296, 74, 64, 2, 1024, 128, 0), (200, 1, 128, 1, 1024, 128, 0),
+             (512, 8, 64, 2, 0, 1024, 4)]
+    steps += [(n, B, H, mn, e, W, 0) for n in (1, 33, 200, 296, 512, 1000, 4096) for B in (1, 8, 74, 200) for H in (1, 8, 64, 128)
+              for mn in (0, 1, 2, 7, 64) for e in (0, 1024, 65536) for W in (1, 128, 1024)]
+    split = 0
+    for n, B, H, mn, e, W, first in steps:
+        got = size(n, B, H, L128, mn, e, W, first)
+        if got == 0:
+            continue
+        split += 1
+        one = [(n * H // R + B) * R * (128 * 2 + 8) for R in (16, 64)]
+        assert any((got - 256) % o == 0 and 2 <= (got - 256) // o <= 64 for o in one), (n, B, H, mn, e, W, first)
+    assert split > 100
