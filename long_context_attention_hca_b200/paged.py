@@ -134,6 +134,8 @@ class PagePlan:
         _want(dev, (self.row_start, _INT, (None if B is None else B + 1,), "plan.row_start"),
               (self.row_req, _INT, (n,), "plan.row_req"), (self.row_pos, _INT, (n,), "plan.row_pos"),
               (self.slot, _LONG, (n,), "plan.slot"))
+        if s.shape[0] == 0:                      # (its last element is the count of live rows)
+            raise ValueError("plan.row_start: must hold B + 1 offsets")
 
 
 def kv_page_plan(ctx_len, new_len, m: int, page_size: int, block_table, free_pages, free_count, plan=None,

@@ -147,3 +147,19 @@ def test_every_split_has_rows_of_a_joined_tile(lib):
         one = [(n * H // R + B) * R * (128 * 2 + 8) for R in (16, 64)]
         assert any((got - 256) % o == 0 and 2 <= (got - 256) // o <= 64 for o in one), (n, B, H, mn, e, W, first)
     assert split > 100
+
+
+def test_a_plan_without_row_starts_is_refused():
+    """row_start holds B + 1 offsets, one at least: with none, the count of live
+    rows would be read in front of it."""
+    import torch
+
+    hca = pytest.importorskip("long_context_attention_hca_b200")
+    cpu = torch.device("cpu")
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    rows = (i32(3), i32(3), torch.zeros(3, dtype=torch.int64))
+    hca.PagePlan(i32(1), *rows).check(cpu)
+    hca.PagePlan(i32(5), *rows).check(cpu, 4)
+    for starts, B in ((i32(0), None), (i32(0), 0), (i32(4), 4), (i32(0).long(), None)):
+        with pytest.raises((ValueError, TypeError)):
+            hca.PagePlan(starts, *rows).check(cpu, B)
