@@ -912,14 +912,16 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             float2 cs = make_float2(1.0f, 0.0f);
             const float2* row_cs = s.cs + (I.tok_row + tok) * 32;
             if (rot && one_tok) cs = row_cs[lane];
-            bar_sync(5, NSOFT * 32);                 // c.mx is read: the next item may write it
+            const int64_t row_out = (parts ? static_cast<int64_t>(it) * PAIR : T.row0) + rbase;
+            // c.mx is read: the next item may write it; and so is this item (soft_item), whose place the item after the
+            // next one takes: with few rows and short key lists no barrier of all eight warps comes before that
+            bar_sync(5, NSOFT * 32);
             // O: row r, dims 256 hk + 128 g .. + 127, 32 of them at a time.  64 rows (always, with 64 heads; partials
             // always): through the P buffers (free now) in turn, four blocks of 64 rows x 32 dims (64-byte swizzle) each
             // stored by one TMA copy while the next 32 dims are read and rounded.  Fewer rows: straight from registers,
             // 32 bytes (a sector) a store where the output allows it (for all rows, that kept the load/store unit busy
             // for 4K clocks an item, and the next item's query conversion waiting).
             const bool whole = parts || rows == ROWS;
-            const int64_t row_out = parts ? static_cast<int64_t>(it) * PAIR + rbase : T.row0 + rbase;
             uint16_t* dst = (parts ? p.part_o : p.out) + (row_out + r) * D + hk * 256 + g * 128;
             uint8_t* seg = smem + P_OFF + (hk * 2 + g) * 4096 + r * 64;
             const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;     // (the same for every row)

@@ -948,3 +948,20 @@ def test_padded_steps_write_every_live_row(k):
     got = c.run(out=out, max_new=mn)
     assert torch.all(got[c.N:] == 7.0) and got.shape[0] == n
     c.check(got, rows=[r for r in range(c.N) if r < 40 or r % 9 == 0 or r == c.N - 1])
+
+
+# ------------------------------------------------------------------ d = 512, many short items of few rows
+@pytest.mark.parametrize("H,new", [(5, 1), (64, 1), (7, 9)])
+def test_many_items_of_one_key_tile(H, new):
+    """Hundreds of items of fewer than 64 rows a CTA and one key tile each, so
+    that a pair's next item starts while parts of the last one are still being
+    written: the same bytes every time, and every request's rows in its place."""
+    r = np.random.default_rng(11)
+    ctx = r.integers(0, 60, 700).tolist()
+    c = Case(512, H, ctx, [new] * 700, 33, n_first=4, PT=8, extras=True, seed=80)
+    want = c.run(max_new=new)
+    c.check(want, rows=set(r.integers(0, c.N, 60).tolist()))
+    for _ in range(30):
+        out = torch.full_like(c.q, 7.0)
+        c.run(max_new=new, out=out)
+        assert torch.equal(out[:c.N], want[:c.N]) and torch.all(out[c.N:] == 7.0)
