@@ -546,7 +546,12 @@ typedef struct {
  *   slot        int64 [max_rows] out: row of the pool where the item goes,
  *               page * page_size + item % page_size; -1 without a page (none
  *               left, or beyond the table's width)
- *   missing     int32 [1] out: pages that could not be given (0: all is well)
+ *   missing     int32 [1] out: pages that the step's items need and do not have
+ *               (0: every row has a slot): new ones that could not be given, and
+ *               those that an earlier step could not get and that have an item in
+ *               this one.  Such a page stays missing until the request starts again:
+ *               its earlier items are lost.  A step that was only planned can be
+ *               planned again with the same ctx_len once pages are free
  *   free_left   int32 [1] out: free pages left (the next step's free_count;
  *               not the same address)
  * Rows row_start[B] .. max_rows - 1 are left as they were; rows beyond

@@ -27,6 +27,11 @@ namespace {
 // table columns that this step does not write, and the free count left is a
 // separate output.  Measured (in a graph): 32 requests of one token 3.8 us, 192
 // requests with 46K rows 5.0 us.
+//
+// Pages missing: new ones that the stack or the table's width does not give, and
+// pages begun in an earlier step that got none then, where this step has an item
+// in them (no fresh page takes their place: the page's earlier items are lost,
+// and a page that lacks them must not become visible).
 constexpr int kPlanThreads = 512;
 constexpr int kPlanMaxB = 16384;            // the C ABI's bound
 
@@ -72,10 +77,16 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
     int32_t* s_page = sh + a.B + 1;         // [B + 1]
     __shared__ int64_t s_warp[3][kPlanThreads / 32];
     __shared__ int64_t s_carry[3];          // rows, pages inside the table, pages wanted
+    __shared__ int s_gone;                  // pages begun earlier that the step needs and no one has
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t P = a.P, width = a.width;
     if (tid < 3) s_carry[tid] = 0;
+    if (tid == 0) s_gone = 0;
     __syncthreads();
+    // counted by the last CTA, which has the fewest rows; a load is waited for in the next round, or at the end
+    const bool counts = blockIdx.x == gridDim.x - 1;
+    int gone = 0;
+    int32_t held = 0;
     for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
         const int b = b0 + tid;
         int64_t v[3] = {0, 0, 0};
@@ -85,6 +96,12 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
             v[0] = s.hi - s.lo;
             v[1] = min(want, width) - min(have, width);
             v[2] = want - have;
+            if (counts) {
+                gone += held < 0;
+                held = 0;
+                if (s.hi > s.lo && s.lo % P != 0)
+                    held = have > width ? -1 : a.table[static_cast<size_t>(b) * width + have - 1];
+            }
         }
         int64_t inc[3] = {v[0], v[1], v[2]};
 #pragma unroll
@@ -145,9 +162,13 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
         a.table[static_cast<size_t>(b) * width + pi] = fresh(k);
     }
     for (int64_t b = gtid; b <= a.B; b += gsz) a.row_start[b] = s_row[b];
-    if (gtid == 0) {
+    if (!counts) return;
+    gone += held < 0;
+    if (gone) atomicAdd(&s_gone, gone);
+    __syncthreads();
+    if (tid == 0) {
         const int64_t granted = min(s_carry[1], static_cast<int64_t>(F));
-        *a.missing = static_cast<int32_t>(min(s_carry[2] - granted, static_cast<int64_t>(0x7FFFFFFF)));
+        *a.missing = static_cast<int32_t>(min(s_carry[2] - granted + s_gone, static_cast<int64_t>(0x7FFFFFFF)));
         *a.free_left = F - static_cast<int32_t>(granted);
     }
 }

@@ -146,7 +146,8 @@ def kv_page_plan(ctx_len, new_len, m: int, page_size: int, block_table, free_pag
     stack with free_count int32 [1] numbers in use (neither is changed:
     plan.free_left is the next step's count).  plan: buffers to write
     (PagePlan.empty), or None with max_rows.  plan.missing counts pages that
-    could not be given; their rows have slot -1."""
+    the step's rows need and do not have, now or since an earlier step; such
+    rows have slot -1."""
     dev = _device(ctx_len, "ctx_len")
     B = ctx_len.shape[0]
     if plan is None:

@@ -639,7 +639,7 @@ class PagedLoop:
         self.token_plan = PagePlan.empty(B, max_rows, dev)
         # every request may complete a block with its first new token
         self.entry_plan = PagePlan.empty(B, B + max_rows // HCA_RATIO, dev)
-        self.short = torch.zeros((1,), **i32)            # pages that could not be given, over all steps
+        self.short = torch.zeros((1,), **i32)            # pages that rows needed and did not have, over all steps
         self.layers: List[PagedLayer] = []
         for li, r in enumerate(ratios):
             P = s9[li] if s9 is not None else None
@@ -689,8 +689,10 @@ class PagedLoop:
         return outs
 
     def missing(self) -> int:
-        """Pages that the steps so far wanted and the pools could not give (the
-        tokens and entries without a page are not visible).  Synchronises."""
+        """Pages that the steps so far needed and the pools could not give, counted
+        in every step with a token or entry in them: those are not visible and
+        not kept, so a request that lost some has to be released and started
+        again.  Synchronises."""
         return int(self.short.item())
 
     def release(self, b: int):

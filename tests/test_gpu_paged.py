@@ -965,3 +965,65 @@ def test_many_items_of_one_key_tile(H, new):
         out = torch.full_like(c.q, 7.0)
         c.run(max_new=new, out=out)
         assert torch.equal(out[:c.N], want[:c.N]) and torch.all(out[c.N:] == 7.0)
+
+
+# ------------------------------------------------------------------ steps after a shortage of pages
+@pytest.mark.parametrize("m", [1, 4])
+def test_a_page_still_missing_is_counted_in_every_step_that_needs_it(m):
+    """Items whose page an earlier step could not get have no slot, and the plan says so: 0 missing means that every
+    row has a slot."""
+    P, width = 4, 3
+    t = torch.full((4, width), -1, dtype=torch.int32, device=DEV)
+    t[3] = i32([0, 1, 2])
+    free, ctx = i32([7, 9]), np.array([0, 0, 0, 10])
+    #        first items of three pages, one of them without; inside them; inside and on; none; past the table's width
+    steps = [([2, 1, 3, 1], [9, 7, -1], 1, 0), ([1, 2, 0, 0], [9, 7, -1], 0, 0), ([0, 0, 1, 0], [9, 7, -1], 1, 0),
+             ([1, 1, 1, 1], [9, 7, -1], 1, 0), ([1, 0, 0, 1], [9, 7, -1], 2, 0), ([0, 0, 1, 1], [9, 7, -1], 2, 0)]
+    count = i32([2])
+    for new, first, missing, left in steps:
+        new = np.array(new)
+        plan = hca.kv_page_plan(i32(ctx * m), i32(new * m), m, P, t, free, count, max_rows=16)
+        assert t[:3, 0].tolist() == first and plan.missing.item() == missing and plan.free_left.item() == left
+        n = int(new.sum())
+        assert (missing == 0) == bool((plan.slot[:n] >= 0).all())
+        count, ctx = plan.free_left, ctx + new
+
+
+def test_many_requests_with_pages_missing():
+    """Every request stands in a page: of 3000, those whose page is gone and that have an item this step are counted."""
+    B, P = 3000, 16
+    r = np.random.default_rng(2)
+    ctx, new = r.integers(1, 64, B), r.integers(0, 3, B)
+    ctx[ctx % P == 0] += 1
+    table = np.arange(B * 6).reshape(B, 6).astype(np.int32)
+    gone = r.random(B) < 0.3
+    table[gone, ctx[gone] // P] = -1 - r.integers(0, 5, int(gone.sum()))
+    plan = hca.kv_page_plan(i32(ctx), i32(new), 1, P, i32(table), i32(np.arange(B) + B * 6), i32([B]), max_rows=2 * B)
+    assert plan.missing.item() == int((gone & (new > 0)).sum()) > 300
+
+
+def test_a_plan_with_pages_missing_can_be_made_again():
+    """Nothing is consumed by a plan: the same lengths again, once pages are free, give every row its slot."""
+    t = torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
+    free, ctx, new = torch.zeros(8, dtype=torch.int32, device=DEV), i32([0, 0]), i32([6, 3])
+    free[0] = 5
+    a = hca.kv_page_plan(ctx, new, 1, 4, t, free, i32([1]), max_rows=9)
+    assert a.missing.item() == 2 and t.tolist() == [[5, -1, -1], [-1, -1, -1]]
+    free[1:3] = i32([2, 3])
+    b = hca.kv_page_plan(ctx, new, 1, 4, t, free, i32([3]), max_rows=9)
+    assert b.missing.item() == 0 and b.free_left.item() == 0 and t.tolist() == [[3, 2, -1], [5, -1, -1]]
+    assert b.slot.tolist() == [12, 13, 14, 15, 8, 9, 20, 21, 22]
+
+
+def test_the_loop_reports_every_step_that_loses_tokens():
+    from long_context_attention_hca_b200.pipeline import PagedLoop
+    d, H = 128, 8
+    g = gen(5)
+    loop = PagedLoop(2, H, LAYOUTS[d], [0], 32, 0, max_tokens=64, max_rows=64, softmax_scale=d ** -0.5, token_page=16,
+                     token_pages=1)
+    seen = []
+    for lens in ([3, 2], [1, 0], [0, 1], [1, 1]):
+        n = sum(lens)
+        loop.step(i32(lens), [bf((n, d), g)], [None], [bf((n, H, d), g)])
+        seen.append(loop.missing())
+    assert seen == [1, 1, 2, 3]
