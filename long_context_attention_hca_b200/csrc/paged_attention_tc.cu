@@ -44,8 +44,9 @@
 // CTA also the item counter), 9 QK issue, 10 PV issue (the first CTA's only),
 // 11-14 query rows to fp16, 15 V copies.  The online softmax is in base 2; O is rescaled only when
 // a row's maximum grows by more than 2^8 (P <= 2^8 in fp16).  Every wait is
-// bounded: one that gives up sets the device error word, the CTA's outputs
-// become NaN, and the pair still meets at the end.
+// bounded: one that gives up sets the device error word, and the pair, which
+// still meets at the end, makes the rows NaN of every item that it was at and of
+// those that no pair has taken (fail_items).
 #include <cuda.h>
 
 #include "paged_attention.cuh"
@@ -361,6 +362,10 @@ struct Item {
     int64_t tok_row;            // row of the request's first new token
 };
 
+// A pair's items that may not be out yet: item j is drawn once j - 1 is posted, that is once all have taken j - 3, and
+// the softmax warps take an item ahead of the output of the one before: j - 4 .. j at most.
+constexpr int RECENT = 8;
+
 struct Ctrl {
     uint64_t full[NSLOT], empty[NSLOT], s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free;
     uint64_t item_full[2], item_free[2], drain;
@@ -368,6 +373,7 @@ struct Ctrl {
     float mx[2][2][ROWS];       // [group][key half][row]: a tile's largest raw logit; at the end each thread's l
     float m[2][ROWS];           // [tile parity]: the running maximum (base 2) after the tile
     Item soft_item[2];          // the softmax warps' copy, by item parity
+    int recent[RECENT];         // the first CTA's: the items with keys that it drew last, in turn (-1: none)
     uint32_t tmem;
     int abort_flag;
 };
@@ -418,6 +424,37 @@ __device__ __forceinline__ bool copy_pieces(Ctrl& c, int slot0, int u, bool firs
     return true;
 }
 
+// After a wait has given up (both CTAs' writes are done): NaN for all rows of the items that the pair drew last, done or
+// not, and of those left on the counter.  Whole warps, each an item at a time.
+__device__ __forceinline__ void fail_items(const Params& p, const Stage& s, const int* recent) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();                                     // (the counter is set)
+    for (bool own = warp < RECENT;; own = false) {
+        int it = 0;
+        if (own) {
+            it = recent[warp];
+            if (it < 0) continue;
+        } else {
+            if (lane == 0) it = atomicAdd(s.next, 1);
+            it = __shfl_sync(0xffffffffu, it, 0);
+            if (it >= s.n_items) break;
+        }
+        Item I;
+        if (!make_item(p, s, it, I)) continue;
+        if (p.n_splits > 1) {
+            // (a weight of NaN: the combine makes the row NaN, whatever else it joins)
+            float* ml = p.part_ml + static_cast<int64_t>(it) * 2 * PAIR;
+            for (int r = lane; r < PAIR; r += 32) {
+                ml[r] = 0.0f;
+                ml[PAIR + r] = __int_as_float(0x7fc00000);
+            }
+        } else {
+            uint4* row = reinterpret_cast<uint4*>(p.out + I.T.row0 * D);
+            for (int i = lane; i < I.T.rows * (D / 8); i += 32) row[i] = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
+        }
+    }
+}
+
 // first staged row of a half tile (past the last: finite rows that no query sees)
 __device__ __forceinline__ int64_t half_row(const Item& I, int h) {
     if (h < I.h_e) return I.ent0 + h * HALF;
@@ -449,6 +486,7 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         mbar_init(smem_u32(&c.q_free), 1);
         mbar_init(smem_u32(&c.o_free), 2 * NSOFT);
         mbar_init(smem_u32(&c.drain), 2);               // both issuing threads
+        for (int i = 0; i < RECENT; ++i) c.recent[i] = -1;
         c.abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -492,7 +530,10 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 J.index = -1;
                 if (it >= s.n_items) break;
                 if (!make_item(p, s, it, J)) continue;
-                if (J.n > 0) break;
+                if (J.n > 0) {
+                    if (lane == 0) c.recent[k & (RECENT - 1)] = it;
+                    break;
+                }
                 // no key tile left for this split: its rows' partials weigh nothing
                 for (int r = lane; r < PAIR; r += 32) {
                     p.part_ml[static_cast<int64_t>(it) * 2 * PAIR + r] = -INFINITY;
@@ -901,11 +942,10 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
             if (parts && hk == 0 && g == 0) {
                 float* ml = p.part_ml + static_cast<int64_t>(it) * 2 * PAIR + rbase + r;
                 ml[0] = m_used;
-                ml[PAIR] = *abort_flag ? __int_as_float(0x7fc00000) : l;
+                ml[PAIR] = l;
             }
             if (!parts && p.sink && (m_used != -INFINITY || l != l)) l += ex2(__ldg(p.sink + (T.r0 + rt) % p.H) * LOG2E - m_used);
-            float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (*abort_flag) inv = __int_as_float(0x7fc00000);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             // RoPE back: pair `lane` at this row's position, when the warp's rows are one token's
             const bool rot = !parts && p.inv_freq && hk == 1 && g == 1;      // this warp holds the RoPE dims
             const bool one_tok = __all_sync(0xffffffffu, tok == __shfl_sync(0xffffffffu, tok, 0));
@@ -996,7 +1036,11 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
         while (!mbar_try(smem_u32(&c.drain), 0) && clock64() - t0 < WAIT_CLOCKS) {}
         __syncwarp();
     }
+    // (what this thread has set, the first CTA knows after the barrier)
+    if (*abort_flag) asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(in_first(smem_u32(&c.abort_flag))), "r"(1) : "memory");
+    __syncwarp();
     cluster_sync();
+    if (rank == 0 && *abort_flag) fail_items(p, s, c.recent);
     if (warp == 9) {
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(TMEM_COLS) : "memory");
