@@ -601,7 +601,8 @@ int kv_page_compress(int32_t m, const uint16_t* x, const uint16_t* gate, int64_t
  * and entries are in their pages already.  A key whose page the map does not
  * hold is not visible; a query that sees no key gets 0.  A key that holds an
  * infinity or a NaN (or a value beyond fp16's range, 65504) makes the outputs
- * of the queries that see it NaN, and of no other.
+ * of the queries that see it NaN, and of no other.  A query that holds such a
+ * value (after its norm and rotation) and sees a key gets NaN.
  *   q, out    bf16 [n_rows][H][d]; rows >= row_start[B] are left as they were
  *   max_new   host bound of a request's new tokens (it chooses the kernels;
  *             a wrong bound costs speed, not results); 0: n_rows

@@ -39,7 +39,9 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
 //
 // A key that holds an infinity or a NaN (or a value beyond fp16's range) is
 // stored as zeros and marked: a query that sees it gets NaN, one that does not
-// see it is untouched (0 x NaN would not be).
+// see it is untouched (0 x NaN would not be).  A query with such a value is NaN
+// throughout: as an infinity it could leave all its logits at -inf, and the row
+// would look like one without keys.
 template <int D, int R>
 struct Rows {
     static constexpr int RG = R / 16, KG = 8 / RG;
@@ -242,6 +244,9 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
         uint32_t h2[CL / 2];
 #pragma unroll
         for (int i = 0; i < CL / 2; ++i) h2[i] = pack_half2(f[2 * i], f[2 * i + 1]);
+        if (__any_sync(0xffffffffu, any_bad(h2)))
+#pragma unroll
+            for (int i = 0; i < CL / 2; ++i) h2[i] = 0x7FFF7FFFu;
         if constexpr (CL >= 8) {
 #pragma unroll
             for (int i = 0; i < CL / 8; ++i)
@@ -284,7 +289,7 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] = bf16x2_to_f16x2(w[i]);
             }
-            const bool bad = here && any_bad16(h);
+            const bool bad = here && any_bad(h);
             // the UPK lanes of a key are one warp's (8 or 32 consecutive lanes)
             const unsigned bm = __ballot_sync(0xffffffffu, bad) >> (UPK == 32 ? 0 : (lane / UPK) * UPK);
             const bool kbad = (bm & (UPK == 32 ? 0xffffffffu : (1u << (UPK & 31)) - 1u)) != 0;
@@ -331,7 +336,9 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int key = k0 + j * 8 + q4 * 2 + (i & 1);
-                            s[j][i] = sees(rk[i >> 1], T.n_e, t * TK + key) ? s[j][i] + s_add[key] : -INFINITY;
+                            // (no such key: -inf for a query of NaN, too)
+                            const float add = s_add[key];
+                            s[j][i] = sees(rk[i >> 1], T.n_e, t * TK + key) && add != -INFINITY ? s[j][i] + add : -INFINITY;
                         }
                 float alpha[2], ref[2], rs[2] = {0.0f, 0.0f};
 #pragma unroll
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(256, D == 512 ? 1 : 2) paged_rows_kernel(Param
                 for (int i = 0; i < 4; ++i) {
                     const int key = kg * C::KEYS + j * 8 + q4 * 2 + (i & 1);
                     float v = s[j][i] * p.scale_log2;
-                    if (flagged) v += s_add[key];
+                    if (flagged) v = s_add[key] == -INFINITY ? -INFINITY : v + s_add[key];
                     if (!sees(rk[i >> 1], T.n_e, t * TK + key)) v = -INFINITY;
                     s[j][i] = v;
                     mx[i >> 1] = fmaxf(mx[i >> 1], v);

@@ -162,12 +162,13 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     return r;
 }
 
-// Whether any of these 16 fp16 values is an infinity or a NaN: x * 0 is then a
+// Whether any of these fp16 pairs holds an infinity or a NaN: x * 0 is then a
 // NaN and stays one in the sum, and +-0 otherwise.
-__device__ __forceinline__ bool any_bad16(const uint32_t (&h)[8]) {
+template <int N>
+__device__ __forceinline__ bool any_bad(const uint32_t (&h)[N]) {
     uint32_t z = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(h[i]), "r"(0u));
+    for (int i = 0; i < N; ++i) asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(z) : "r"(h[i]), "r"(0u));
     return (z & 0x7FFF7FFFu) != 0;
 }
 

@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(256) stage_kernel(Params p, Stage s) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) h[i] = pack_half2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xFFFF0000u));
             }
-            const bool bad = __any_sync(0xffffffffu, any_bad16(h));
+            const bool bad = __any_sync(0xffffffffu, any_bad(h));
             const uint32_t keep = bad ? 0u : 0xffffffffu;
             uint4* dst = reinterpret_cast<uint4*>(s.rows + (g0 + k0 + k) * D + d0);
             dst[0] = make_uint4(h[0] & keep, h[1] & keep, h[2] & keep, h[3] & keep);
@@ -894,7 +894,8 @@ paged_tc_kernel(Params p, Stage s, const __grid_constant__ CUtensorMap k_map, co
                 const float2 pt = unpair(add2(add2(ps[0], ps[1]), add2(ps[2], ps[3])));
                 l_run = (m_l == -INFINITY ? l_run : l_run * ex2(m_l - m_new)) + (pt.x + pt.y);
                 m_l = m_new;
-                if (bad) l_run = __int_as_float(0x7fc00000);             // a visible key that is not finite
+                // a visible key that is not finite; or a query that is not, and all its logits so far -inf
+                if (bad || (m_new == -INFINITY && (vis[0] | vis[1]))) l_run = __int_as_float(0x7fc00000);
                 if (use > 0 && ok) ok = wait_bar(smem_u32(&c.pv_done[g]), (use - 1) & 1, abort_flag);   // P's buffer is free
                 if (__any_sync(0xffffffffu, resc)) {
                     // O must hold still: PV(i - 1) complete (the barrier's phase before belongs to a PV that completed

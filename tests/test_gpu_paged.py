@@ -1027,3 +1027,45 @@ def test_the_loop_reports_every_step_that_loses_tokens():
         loop.step(i32(lens), [bf((n, d), g)], [None], [bf((n, H, d), g)])
         seen.append(loop.missing())
     assert seen == [1, 1, 2, 3]
+
+
+# ------------------------------------------------------------------ queries beyond fp16's range
+FAR = [(dict(d=512, H=64, ctx=[400, 0, 30], new=[3, 1, 2], W=20, m=4), 6), (dict(d=512, H=5, ctx=[400, 0, 30], new=[30, 1, 2], W=20), 0),
+       (dict(d=512, H=64, ctx=[30000, 100], new=[1, 1], W=128, m=4, PE=32), 1),
+       (dict(d=128, H=8, ctx=[400, 0, 30], new=[1, 1, 1], W=20, m=4), 1), (dict(d=128, H=64, ctx=[400, 0, 30], new=[3, 1, 2], W=20, m=4), 3),
+       (dict(d=128, H=64, ctx=[9000, 100], new=[1, 1], W=128, m=4), 1), (dict(d=128, H=128, ctx=[90, 700], new=[150, 170], W=17, m=4), 0)]
+
+
+@pytest.mark.parametrize("value", [float("inf"), 1e5, float("nan")])
+@pytest.mark.parametrize("sink", [False, True])
+@pytest.mark.parametrize("k,wide", [(k, False) for k in range(len(FAR))] + [(0, True), (2, True)])     # (wide: not staged)
+def test_a_query_beyond_fp16_is_nan_whatever_its_keys(k, wide, value, sink):
+    """Every visible key's product with the far element is negative: no logit is
+    finite, and none is +inf.  The row is NaN, not the 0 of a row without keys,
+    and the others' bytes do not change; a row that sees no key is 0."""
+    kw, mn = FAR[k]
+    c = Case(seed=90, **kw)
+    if sink:
+        c.ex = hca.AttnExtras(None, 1e-6, torch.zeros(c.H, device=DEV), None)
+    at = c.d - 1                                         # a dim that entries hold in bf16
+    c.pages[..., at] = -c.pages[..., at].abs() - 2.0 ** -14
+    if c.cache is not None:
+        c.cache.rope[..., -1] = -c.cache.rope[..., -1].abs() - 2.0 ** -14
+    if wide:
+        t = torch.full((len(c.ctx), (3 << 20) // c.PE), -1, dtype=torch.int32, device=DEV)
+        t[:, :c.ew] = c.etab
+        c.etab = t
+    clean = c.run(max_new=mn)
+    hit = torch.zeros((c.N, c.H), dtype=torch.bool, device=DEV)
+    for b in range(len(c.ctx)):
+        for n in {int(c.starts[b]), int(c.starts[b + 1]) - 1}:
+            hit[n, (3 * n + 1) % c.H] = True
+    c.q[:c.N, :, at][hit] = value
+    got = c.run(max_new=mn)
+    assert torch.isnan(got[:c.N][hit]).all()
+    assert torch.equal(got[:c.N][~hit], clean[:c.N][~hit])
+    c.ttab[:] = -1
+    if c.cache is not None:
+        c.etab[:] = c.cache.B
+    assert torch.all(c.run(max_new=mn)[:c.N] == 0)
+    assert hca.take_device_error() == 0
