@@ -125,7 +125,15 @@ class PagePlan:
         zero = lambda n: torch.zeros((n,), dtype=_INT, device=device)
         return cls(zero(B + 1), full(max_rows, _INT), full(max_rows, _INT), full(max_rows, _LONG), zero(1), zero(1))
 
-    def check(self, dev, B=None):
+    def check(self, dev, B=None, totals=False):
+        """The buffers' types, sizes (of B requests) and device; totals: missing
+        and free_left, which kv_page_plan writes, too."""
+        if totals:
+            for t, name in ((self.missing, "plan.missing"), (self.free_left, "plan.free_left")):
+                if t is None:
+                    raise ValueError(f"{name}: is needed to make a plan (int32 [1])")
+                if not _ok(t, _INT, (1,), dev):
+                    _want(dev, (t, _INT, (1,), name))
         n = self.slot.shape[0]
         s = self.row_start
         if (_ok(self.slot, _LONG, (n,), dev) and _ok(self.row_pos, _INT, (n,), dev) and _ok(self.row_req, _INT, (n,), dev)
@@ -157,13 +165,11 @@ def kv_page_plan(ctx_len, new_len, m: int, page_size: int, block_table, free_pag
             plan = PagePlan.empty(B, max_rows, dev)
     width, n_free = block_table.shape[-1], free_pages.shape[0]
     if not (_ok(ctx_len, _INT, (B,), dev) and _ok(new_len, _INT, (B,), dev) and _ok(block_table, _INT, (B, width), dev)
-            and _ok(free_pages, _INT, (n_free,), dev) and _ok(free_count, _INT, (1,), dev)
-            and _ok(plan.missing, _INT, (1,), dev) and _ok(plan.free_left, _INT, (1,), dev)):
+            and _ok(free_pages, _INT, (n_free,), dev) and _ok(free_count, _INT, (1,), dev)):
         _want(dev, (ctx_len, _INT, (B,), "ctx_len"), (new_len, _INT, (B,), "new_len"),
               (block_table, _INT, (B, None), "block_table"), (free_pages, _INT, (None,), "free_pages"),
-              (free_count, _INT, (1,), "free_count"), (plan.missing, _INT, (1,), "plan.missing"),
-              (plan.free_left, _INT, (1,), "plan.free_left"))
-    plan.check(dev, B)
+              (free_count, _INT, (1,), "free_count"))
+    plan.check(dev, B, totals=True)
     with _on(dev):
         _check(_lib.kv_page_plan(ctx_len.data_ptr(), new_len.data_ptr(), B, m, page_size, block_table.data_ptr(),
                                  width, free_pages.data_ptr(), free_count.data_ptr(),

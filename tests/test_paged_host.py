@@ -163,3 +163,18 @@ def test_a_plan_without_row_starts_is_refused():
     for starts, B in ((i32(0), None), (i32(0), 0), (i32(4), 4), (i32(0).long(), None)):
         with pytest.raises((ValueError, TypeError)):
             hca.PagePlan(starts, *rows).check(cpu, B)
+
+
+def test_a_plan_to_be_made_needs_its_totals():
+    """What a PagePlan lacks is named before anything runs."""
+    import torch
+
+    hca = pytest.importorskip("long_context_attention_hca_b200")
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    plan = hca.PagePlan(i32(3), i32(3), i32(3), torch.zeros(3, dtype=torch.int64))
+    with pytest.raises(ValueError, match="missing"):
+        plan.check(torch.device("cpu"), 2, totals=True)
+    plan.check(torch.device("cpu"), 2)
+    with pytest.raises(TypeError, match="free_left"):
+        hca.PagePlan(plan.row_start, plan.row_req, plan.row_pos, plan.slot, i32(1), i32(1).long()).check(
+            torch.device("cpu"), 2, totals=True)
