@@ -657,6 +657,35 @@ class PagedLoop:
         """HCA layer li: the compressor's positional bias [128][d]."""
         self.layers[li].bias = bias
 
+    def _check(self, new_len, x_new, gate_new, q, max_new):
+        """All of a step's arguments, before its first launch: a step that broke
+        off between two layers would have moved the first one's tails."""
+        from .paged import _ok, _want
+
+        def want(t, dt, shape, name):
+            if not _ok(t, dt, shape, dev):
+                _want(dev, (t, dt, shape, name))
+
+        dev, n_rows, d = self.ctx.device, self.token_plan.slot.shape[0], self.layout[0]
+        if not len(x_new) == len(gate_new) == len(q) == len(self.layers):
+            raise ValueError("x_new, gate_new, q: one of each for all layers")
+        if max_new is not None and max_new < 0:
+            raise ValueError("max_new: must not be negative")
+        want(new_len, torch.int32, (self.B,), "new_len")
+        for li, L in enumerate(self.layers):
+            n = x_new[li].shape[0]
+            want(x_new[li], torch.bfloat16, (n, d), f"x_new[{li}]")
+            want(q[li], torch.bfloat16, (q[li].shape[0], self.H, d), f"q[{li}]")
+            if n > n_rows:
+                raise ValueError(f"x_new[{li}]: more rows than max_rows")
+            if L.ratio > 0:
+                if L.bias is None:
+                    raise ValueError(f"layer {li}: no positional bias (set_bias)")
+                if gate_new[li] is None:
+                    raise ValueError(f"gate_new[{li}]: is needed by an HCA layer")
+                want(gate_new[li], torch.bfloat16, (n, d), f"gate_new[{li}]")
+                want(L.bias, torch.float32, (L.ratio, d), f"layer {li}'s bias")
+
     def step(self, new_len: torch.Tensor, x_new: List[torch.Tensor], gate_new: List[Optional[torch.Tensor]],
              q: List[torch.Tensor], max_new: Optional[int] = None):
         """One step: new_len int32 [B] on the device; per layer the new tokens'
@@ -665,6 +694,7 @@ class PagedLoop:
         request; max_new: host bound of a request's new tokens.  Returns the
         per-layer outputs [n][H][d]."""
         from . import kv_page_compress, kv_page_plan, kv_page_store, paged_attn_chunk, paged_attn_window
+        self._check(new_len, x_new, gate_new, q, max_new)
         tp, ep = self.token_plan, self.entry_plan
         kv_page_plan(self.ctx, new_len, 1, self.token_page, self.token_table, self.free_tokens, self.n_free_tokens,
                      plan=tp)

@@ -178,3 +178,29 @@ def test_a_plan_to_be_made_needs_its_totals():
     with pytest.raises(TypeError, match="free_left"):
         hca.PagePlan(plan.row_start, plan.row_req, plan.row_pos, plan.slot, i32(1), i32(1).long()).check(
             torch.device("cpu"), 2, totals=True)
+
+
+def test_the_loop_refuses_before_anything_is_launched():
+    """A step's arguments are all looked at before its first call."""
+    import torch
+
+    pytest.importorskip("long_context_attention_hca_b200")
+    from long_context_attention_hca_b200.pipeline import PagedLoop
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)
+    loop = PagedLoop(2, 8, (128, 32, 32), [0, 128], 16, 0, max_tokens=64, max_rows=8, softmax_scale=0.1, token_page=16,
+                     device="cpu")
+    x = torch.zeros((2, 128), dtype=torch.bfloat16)
+    q = torch.zeros((2, 8, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="set_bias"):
+        loop.step(i32(2), [x, x], [None, x], [q, q])
+    loop.set_bias(1, torch.zeros((128, 128)))
+    with pytest.raises(ValueError, match="gate_new"):
+        loop.step(i32(2), [x, x], [None, None], [q, q])
+    for bad in (dict(x_new=[x]), dict(q=[q]), dict(gate_new=[None])):
+        with pytest.raises(ValueError, match="layers"):
+            loop.step(**{**dict(new_len=i32(2), x_new=[x, x], gate_new=[None, x], q=[q, q]), **bad})
+    for bad in (dict(new_len=i32(3)), dict(x_new=[x, x.float()]), dict(x_new=[x, x[:, :64]]), dict(gate_new=[None, x[:1]]),
+                dict(q=[q, q[:, :4]]), dict(max_new=-1), dict(x_new=[torch.zeros((9, 128), dtype=torch.bfloat16), x])):
+        with pytest.raises((ValueError, TypeError)):
+            loop.step(**{**dict(new_len=i32(2), x_new=[x, x], gate_new=[None, x], q=[q, q]), **bad})
+    assert loop.ctx.tolist() == [0, 0] and loop.token_table.eq(-1).all()
