@@ -667,8 +667,8 @@ class PagedLoop:
                 _want(dev, (t, dt, shape, name))
 
         dev, n_rows, d = self.ctx.device, self.token_plan.slot.shape[0], self.layout[0]
-        if not len(x_new) == len(gate_new) == len(q) == len(self.layers):
-            raise ValueError("x_new, gate_new, q: one of each for all layers")
+        if min(len(x_new), len(q)) < len(self.layers):
+            raise ValueError("x_new, q: one of each for all layers")
         if max_new is not None and max_new < 0:
             raise ValueError("max_new: must not be negative")
         want(new_len, torch.int32, (self.B,), "new_len")
@@ -681,7 +681,7 @@ class PagedLoop:
             if L.ratio > 0:
                 if L.bias is None:
                     raise ValueError(f"layer {li}: no positional bias (set_bias)")
-                if gate_new[li] is None:
+                if gate_new is None or li >= len(gate_new) or gate_new[li] is None:
                     raise ValueError(f"gate_new[{li}]: is needed by an HCA layer")
                 want(gate_new[li], torch.bfloat16, (n, d), f"gate_new[{li}]")
                 want(L.bias, torch.float32, (L.ratio, d), f"layer {li}'s bias")

@@ -196,11 +196,18 @@ def test_the_loop_refuses_before_anything_is_launched():
     loop.set_bias(1, torch.zeros((128, 128)))
     with pytest.raises(ValueError, match="gate_new"):
         loop.step(i32(2), [x, x], [None, None], [q, q])
-    for bad in (dict(x_new=[x]), dict(q=[q]), dict(gate_new=[None])):
-        with pytest.raises(ValueError, match="layers"):
+    for bad in (dict(x_new=[x]), dict(q=[q]), dict(gate_new=[None]), dict(gate_new=None)):
+        with pytest.raises(ValueError, match="layer"):
             loop.step(**{**dict(new_len=i32(2), x_new=[x, x], gate_new=[None, x], q=[q, q]), **bad})
     for bad in (dict(new_len=i32(3)), dict(x_new=[x, x.float()]), dict(x_new=[x, x[:, :64]]), dict(gate_new=[None, x[:1]]),
                 dict(q=[q, q[:, :4]]), dict(max_new=-1), dict(x_new=[torch.zeros((9, 128), dtype=torch.bfloat16), x])):
         with pytest.raises((ValueError, TypeError)):
             loop.step(**{**dict(new_len=i32(2), x_new=[x, x], gate_new=[None, x], q=[q, q]), **bad})
     assert loop.ctx.tolist() == [0, 0] and loop.token_table.eq(-1).all()
+    # gates are asked for HCA layers only
+    first = PagedLoop(2, 8, (128, 32, 32), [128, 0], 16, 0, max_tokens=64, max_rows=8, softmax_scale=0.1, device="cpu")
+    first.set_bias(0, torch.zeros((128, 128)))
+    first._check(i32(2), [x, x], [x], [q, q], None)
+    window = PagedLoop(2, 8, (128, 32, 32), [0], 16, 0, max_tokens=64, max_rows=8, softmax_scale=0.1, device="cpu")
+    for gates in (None, [], [None]):
+        window._check(i32(2), [x], gates, [q], 1)
