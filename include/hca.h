@@ -172,7 +172,8 @@ int hca_compress(const uint16_t* x, const uint16_t* gate, int64_t x_seq_stride,
  * Arithmetic (fixed so stored codes stay bit-exact): the squares are rounded
  * and summed as a pairwise tree over consecutive channel pairs, r =
  * sqrt(sum / d + eps) correctly rounded, y = (y / r) * w in fp32.  RoPE:
- * the angle position * inv_freq[i] in fp64 (exact), the rotation
+ * the angle position * inv_freq[i] in fp64 (one product, exact for positions
+ * below 2^29), the rotation
  * (a cos - b sin, a sin + b cos) in fp64 with every product and sum rounded,
  * then one rounding to bf16.  A compressed entry e of ratio m sits at
  * position e * m (its block's first token). */

@@ -55,7 +55,7 @@ __device__ __forceinline__ void rms_norm8(float (&y)[8], const float* __restrict
 }
 
 //  - Partial RoPE of the thread's 4 channel pairs (2i, 2i+1) of the RoPE
-//    dims, rotated to position pos by the angle pos * inv_freq[i] (an exact
+//    dims, rotated to position pos by the angle pos * inv_freq[i] (the
 //    fp64 product), in fp64 with every product and sum rounded (no FMA), then
 //    rounded once to bf16 (4 bf16x2 words out).
 __device__ __forceinline__ void rope8_to_bf16(const float (&y)[8], int pair0, int64_t pos,

@@ -34,7 +34,7 @@ int tc_chunk_launch(const Params& p, int64_t tiles, int64_t max_entries, void* w
 // Bound at d = 128: latency and issue, not bytes.  A 64-key tile of R = 128 takes
 // 9.3K clocks with one CTA an SM (1.5K converting keys, 1.1K queueing copies,
 // 2.1K S, 4.1K softmax and O) and 11K with two, 4096 tokens x 64 heads over 64K
-// take 509 us, 171 TFLOP/s; 33 single tokens of 8 heads, 10.7 us.  Converting
+// take 493 us, 178 TFLOP/s; 33 single tokens of 8 heads, 10.4 us cold.  Converting
 // from registers a tile ahead and four-warp CTAs, three an SM, were no faster.
 //
 // A key that holds an infinity or a NaN (or a value beyond fp16's range) is
@@ -648,17 +648,19 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(Params p) {
 }
 
 // ---------------------------------------------------------------- host side
-// Staged keys take 1 KB each: at most 2 GB of workspace; beyond that (64
-// requests whose entry tables reach 4M tokens, say) the row kernel serves d =
-// 512 too, several times slower.
+// Staged keys take 1 KB each: at most 2 GB of workspace, by the tables' widths
+// (the lengths are on the device); beyond that (64 requests whose entry tables
+// reach 4M tokens, or 255 that reach 1M) the row kernel serves d = 512 too: 4096
+// tokens after 131072 in 4.24 ms where the pairs take 0.59, 13 mixed requests 1.11
+// and 0.21 ms, 4 single tokens after 1M 49 and 37 us.
 constexpr int64_t MAX_STAGE_ROWS = 2ll << 20;
 constexpr int PAIR_ROWS = 128;
 
 // Rows of a row kernel's tile: 16 when no request can fill more (a small head
 // count at decode); 128 when such tiles give every SM one (500 tokens x 64 heads
-// over 64K: 76 us, with 64 rows 94; 4096 tokens 509 and 650; between one and two
-// tiles an SM either is ahead by turns, 4 x 170 window tokens 63 and 58 us); else
-// 64 (64 tokens over 128K: 35 us; 32 single tokens 23, splits included).  What
+// over 64K: 73 us, with 64 rows 95; 4096 tokens 493 and 660; between one and two
+// tiles an SM either is ahead by turns, 4 x 170 window tokens 47 and 46 us); else
+// 64 (64 tokens over 128K: 35 us; 32 single tokens 22, splits included).  What
 // counts is the rows that can hold a query: a padded step has many others.
 inline int tile_rows(int64_t n_rows, int B, int64_t max_new, int H) {
     if (max_new * H <= 16) return 16;
@@ -702,8 +704,8 @@ static Plan make_plan(int64_t n_rows, int B, int H, int D, int64_t max_new, int6
         k.splits = 1;       // taken only where the tiles alone give every SM one: there is no combine of such tiles
     } else {
         // d = 128: two CTAs fit an SM, where that gives shorter chains and not the same work twice as thin (32 single
-        // tokens x 64 heads over 64K: 22.6 us with both slots counted, 26.1 with one; 100 over 32K: 37 and 30 us, so
-        // not for 64-row tiles that fill more than half the SMs; with 8 heads 16.7 and 20.4)
+        // tokens x 64 heads over 64K: 22.4 us with both slots counted, 26.1 with one; 100 over 32K: 37 and 30 us, so
+        // not for 64-row tiles that fill more than half the SMs; with 8 heads 15.9 and 20.4)
         const bool both = D == 128 && (k.R == 16 || 2 * busy <= sm_count());
         k.splits = split_count(both ? 2 * sm_count() : sm_count(), busy, max_keys, TK, 2);
     }

@@ -197,11 +197,13 @@ __device__ __forceinline__ void dequant16(const uint4& cv, float sc, uint32_t (&
     }
 }
 
-// cos / sin of RoPE pair i at position t, fp32 out.  The angle t f_i is exact in
-// fp64 (31 + 24 bits); its whole half turns are taken off there (the product
-// with 1 / pi is off by 2^-53 of itself: below 2^-24 of a half turn for every
-// position), and the rest, in [-1/2, 1/2] half turns, goes to sincospif.  An
-// fp64 sincos costs 16K clocks of latency here, more than the query's load.
+// cos / sin of RoPE pair i at position t, fp32 out.  The angle t f_i is an fp64
+// product (exact below position 2^29: 29 + 24 bits); its whole half turns are
+// taken off there, and the rest, in [-1/2, 1/2] half turns, goes to sincospif.
+// u = t f_i / pi is off by three roundings (the angle, 1 / pi, the product), 3 x
+// 2^-53 of itself: for f_i <= 1 below 2^-24 of a half turn up to position 2^29
+// and 2^-22 at 2^31, where the query's rounding to fp16 is 2^-11.  An fp64 sincos
+// costs 16K clocks of latency here, more than the query's load.
 __device__ __forceinline__ float2 rope_cs(const float* inv_freq, int i, int64_t t) {
     const double u = static_cast<double>(t) * static_cast<double>(__ldg(inv_freq + i)) * 0.31830988618379067154;
     const double k = rint(u);

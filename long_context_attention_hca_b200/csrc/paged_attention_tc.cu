@@ -22,7 +22,7 @@
 // 2 x 128 columns.
 //
 // Per 128-key tile and CTA: 48 instructions, 2048 clocks at the tensor pipe's
-// rate; shared memory moves 256 KB for QK's operands (1024 clocks at 128 B), 96
+// rate; shared memory moves 128 KB for QK's operands (1024 clocks at 128 B), 96
 // KB for PV's (768) and 128 KB in.  The K and the V part of a tile arrive as four
 // 16 KB pieces each, every piece with its own slot, so that a piece of the next
 // tile is on its way as soon as its predecessor is multiplied; one TMA a piece

@@ -25,8 +25,8 @@ namespace {
 // request by binary search there.  Nothing that a CTA reads is written by
 // another: fresh pages are computed from the free list, old ones are read from
 // table columns that this step does not write, and the free count left is a
-// separate output.  Measured (in a graph): 32 requests of one token 3.8 us, 192
-// requests with 46K rows 5.0 us.
+// separate output.  Measured (in a graph): 32 requests of one token 3.5 us, 192
+// requests with 46K rows 4.6 us.
 //
 // Pages missing: new ones that the stack or the table's width does not give, and
 // pages begun in an earlier step that got none then, where this step has an item
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(PlanArgs a) {
 // and each lane computes the fp64 angle of ONE RoPE pair (the d_rope / 2 pairs
 // over the lanes), where a thread that owns 8 channels would compute four in a
 // row.  Bytes: 4 d + 12 a token.  Measured (in a graph): 14K tokens of d = 512
-// with RMSNorm and RoPE 10.4 us, 2.8 TB/s (42% of a copy); 32 tokens 3.0 us, a
+// with RMSNorm and RoPE 10.0 us, 2.9 TB/s (44% of a copy); 32 tokens 3.0 us, a
 // load, the tree and a store in a row.
 template <int D>
 __global__ void __launch_bounds__(256)

@@ -50,9 +50,9 @@ __device__ __forceinline__ void load8_f32(const float* p, float (&v)[8]) {
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
-// One RoPE pair (a, b) rotated to position pos by the angle pos * f (an exact
-// fp64 product), in fp64 with every product and sum rounded (no FMA), each
-// result rounded once to bf16 (a in the low half).
+// One RoPE pair (a, b) rotated to position pos by the angle pos * f (the fp64
+// product, exact below position 2^29), in fp64 with every product and sum rounded
+// (no FMA), each result rounded once to bf16 (a in the low half).
 __device__ __forceinline__ uint32_t rope_pair_to_bf16(float a_, float b_, int64_t pos, float f) {
     const double ang = __dmul_rn(static_cast<double>(pos), static_cast<double>(f));
     double sn, cs;
@@ -65,12 +65,13 @@ __device__ __forceinline__ uint32_t rope_pair_to_bf16(float a_, float b_, int64_
     return lo | (hi << 16);
 }
 
-// cos and sin of pos * f in fp64, to a few units in its last place: the angle
-// is exact (31 + 24 bits), u = angle / pi is reduced to r in [-1/2, 1/2] by one
-// fused multiply-add (1 / pi in two parts: its nearest double and the rest), and
-// sincospi has no large arguments to look after.  Rounded to bf16 the rotation
-// is that of rope_pair_to_bf16 (the two differ by 2^-50 where bf16 steps by
-// 2^-8), at a fraction of the latency.
+// cos and sin, each within a few 2^-53, of the fp64 product pos * f, which is the
+// angle (exact below position 2^29, rounded beyond, as in rope_pair_to_bf16): u =
+// angle / pi is reduced to r in [-1/2, 1/2] by one fused multiply-add (1 / pi in
+// two parts: its nearest double and the rest), and sincospi has no large
+// arguments to look after.  The rotated pair is that of rope_pair_to_bf16 to
+// about 2^-51 (|a| + |b|), so that its bf16 values are the same unless one lies
+// that near to the middle between two of them; at a fraction of the latency.
 struct CosSin { double c, s; };
 __device__ __forceinline__ CosSin rope_cos_sin(int64_t pos, float f) {
     const double ang = __dmul_rn(static_cast<double>(pos), static_cast<double>(f));
